@@ -238,7 +238,7 @@ def _prepare_own(st):
     case, op = st["case"], st["case"]["op"]
     if op == "roundtrip":
         st["q"] = ne.Mx4.empty(case["rows"], case["cols"], ne.MX4_ROWS)
-        st["ws"] = ne.new_embedding_workspace(case["rows"], case["rows"])
+        st["ws"] = ne.new_embedding_workspace(0, case["cols"])
     elif op == "linear":
         st["q"] = ne.Mx4.empty(case["M"], case["K"], ne.MX4_TILES)
         st["w"] = ne.Mx4(st["w_codes"], _tiles(st["w_scales"]), case["N"], case["K"], ne.MX4_TILES)
@@ -254,7 +254,7 @@ def _prepare_own(st):
     else:
         if op == "lookup" and case["table"] == "mx4":
             st["table"] = ne.Mx4(*st["table"], case["V"], case["D"], ne.MX4_ROWS)
-        st["ws"] = ne.new_embedding_workspace(case["n"], case["V"])
+        st["ws"] = ne.new_embedding_workspace(case["n"], case["D"])
 
 
 # ------------------------------------------------------------------------------ one pass
