@@ -26,7 +26,8 @@ _lib = ctypes.CDLL(LIB_PATH)
 _P = ctypes.c_void_p
 _I32, _I64, _SZ = ctypes.c_int32, ctypes.c_int64, ctypes.c_size_t
 
-NGRAM_BF16, NGRAM_F32 = 0, 1
+NGRAM_BF16, NGRAM_F32, NGRAM_MX4 = 0, 1, 2
+MX4_ROWS, MX4_TILES = 0, 1
 STATUS_BITS = {
     0x1: "BAD_TOKEN", 0x2: "BAD_OFFSETS", 0x4: "BAD_SLOT", 0x8: "BAD_APPEND",
     0x10: "BAD_ROLLBACK", 0x20: "EVICTED", 0x40: "TIMEOUT",
@@ -50,6 +51,9 @@ EXPORTED = [
     "ngram_embed_fwd_step", "ngram_embed_plan_set_dense_a", "ngram_embed_plan_set_pair_columns",
     "ngram_embed_plan_set_fused_step", "ngram_embed_plan_set_backward_pair",
     "ngram_embed_plan_set_backward_streams",
+    "ngram_mx4_scale_bytes", "ngram_mx4_quantize", "ngram_mx4_product_workspace_bytes", "ngram_mx4_product",
+    "ngram_embed_mx4_workspace_bytes", "ngram_embed_fwd_mx4", "ngram_embed_project_mx4",
+    "ngram_embedding_workspace_bytes", "ngram_embedding_fwd", "ngram_embedding_bwd", "ngram_embedding_bwd_rows",
 ]
 
 
@@ -64,6 +68,10 @@ class _Cache(ctypes.Structure):
 
 class _DraftCache(ctypes.Structure):
     _fields_ = [("keys", _P), ("emb", _P), ("positions", _I32), ("max_seqs", _I32)]
+
+
+class _Mx4(ctypes.Structure):
+    _fields_ = [("codes", _P), ("scales", _P)]
 
 
 def _sig(name, args, res=ctypes.c_int):
@@ -113,6 +121,21 @@ _sig("ngram_embed_bwd", [_P, _P, _P, _I64, _P, _P, _P, _P, _P, _P, _P, _SZ, _P])
 _sig("ngram_embed_layernorm", [_P, _P, _I64, _P, _P, ctypes.c_float, _P, _P, _SZ, _P])
 _sig("ngram_embed_selftest_wait_timeout", [_P, _I64, _P])
 _sig("ngram_embed_fwd_static_ws", [_P, _P, _P, _I32, _I64, _P, _P, _P, _P, _P, _P, _P, _P])
+
+_MX = ctypes.POINTER(_Mx4)
+_sig("ngram_mx4_scale_bytes", [_I64, _I64, ctypes.c_int], _SZ)
+_sig("ngram_mx4_quantize", [_P, ctypes.c_int, _I64, _I64, _I64, _P, _P, ctypes.c_int, _P])
+_sig("ngram_mx4_product_workspace_bytes", [_I64, _I64, _I64], _SZ)
+_sig("ngram_mx4_product", [_MX, _MX, _I64, _I64, _I64, ctypes.c_float, _P, ctypes.c_int, _I64, _P, _SZ, _P])
+_sig("ngram_embed_mx4_workspace_bytes", [_P, _I64], _SZ)
+_sig("ngram_embed_fwd_mx4", [_P, _P, _P, _I32, _I64, _P, _MX, _MX, _P, _P, _P, _P, _SZ, _P])
+_sig("ngram_embed_project_mx4", [_P, _P, _P, _I64, _P, _MX, _MX, _P, _P, _SZ, _P])
+_sig("ngram_embedding_workspace_bytes", [_I64, _I64], _SZ)
+_sig("ngram_embedding_fwd", [_P, _P, ctypes.c_int, _I64, _I64, _P, _I64, ctypes.c_float, _I64, _P, ctypes.c_int, _I64,
+                             _P, _SZ, _P])
+_sig("ngram_embedding_bwd", [_P, _I64, _P, ctypes.c_int, _I64, _I64, _I64, ctypes.c_float, _I64, _P, _P, _SZ, _P])
+_sig("ngram_embedding_bwd_rows", [_P, _I64, _P, ctypes.c_int, _I64, _I64, _I64, ctypes.c_float, _I64, _P, _P, _P, _P,
+                                  _SZ, _P])
 
 
 class NgramError(RuntimeError):
@@ -480,3 +503,220 @@ def new_workspace(plan: Plan, max_tokens: int, device="cuda"):
     import torch
     n = ngram_embed_workspace_bytes(plan, max_tokens)
     return torch.zeros(n, dtype=torch.uint8, device=device)
+
+
+# ---- 4-bit tables, and one table's lookup and gradient ----
+
+def _device_stream(stream, t):
+    """The given stream, or the current one of the tensor's own device."""
+    import torch
+    s = stream if stream is not None else torch.cuda.current_stream(t.device)
+    return ctypes.c_void_p(s.cuda_stream)
+
+
+def _bytes_of(t):
+    return t.numel() * t.element_size()
+
+
+def _rows2d(t, name, device=None):
+    """A CUDA bf16 or f32 matrix with dense rows: its dtype code."""
+    import torch
+    code = {torch.bfloat16: NGRAM_BF16, torch.float32: NGRAM_F32}.get(t.dtype)
+    if code is None or not t.is_cuda or t.dim() != 2 or (t.shape[1] > 1 and t.numel() > 0 and t.stride(1) != 1):
+        raise NgramError(f"{name} must be a bf16 or f32 CUDA matrix with dense rows")
+    if device is not None and t.device != device:
+        raise NgramError(f"{name} is on {t.device}, not on {device}")
+    return code
+
+
+def _stride(t):
+    """Row stride in elements (a matrix of at most one row may carry any)."""
+    return max(t.stride(0), t.shape[1]) if t.shape[0] > 1 else t.shape[1]
+
+
+def _on(device, **tensors):
+    for name, t in tensors.items():
+        if t is not None and t.device != device:
+            raise NgramError(f"{name} is on {t.device}, not on {device}")
+
+
+def _ids(t, name, n=None):
+    import torch
+    if t.dtype != torch.int32 or not t.is_cuda or not t.is_contiguous() or (n is not None and t.numel() != n):
+        raise NgramError(f"{name} must be a contiguous int32 CUDA tensor" + ("" if n is None else f" of {n} entries"))
+    return _ptr(t)
+
+
+class Mx4:
+    """A [rows, cols] array in microscaled 4-bit floating point (caller-owned torch tensors):
+    codes uint8 [rows, cols / 2]; scales uint8, [rows, cols / 32] by rows (MX4_ROWS) or a flat
+    array of 512-byte tiles (MX4_TILES)."""
+
+    def __init__(self, codes, scales, rows: int, cols: int, layout: int = MX4_ROWS):
+        import torch
+        need = _lib.ngram_mx4_scale_bytes(int(rows), int(cols), int(layout))
+        if rows < 0 or cols < 1 or cols % 32 != 0 or layout not in (MX4_ROWS, MX4_TILES):
+            raise NgramError("Mx4 needs rows >= 0, columns a multiple of 32 and a known layout")
+        for name, t, n in (("codes", codes, rows * cols // 2), ("scales", scales, need)):
+            if t.dtype != torch.uint8 or not t.is_cuda or not t.is_contiguous() or t.numel() != n:
+                raise NgramError(f"Mx4 {name} must be a contiguous uint8 CUDA tensor of {n} bytes")
+        _on(codes.device, scales=scales)
+        self.codes, self.scales, self.rows, self.cols, self.layout = codes, scales, int(rows), int(cols), int(layout)
+        self.struct = _Mx4(codes.data_ptr(), scales.data_ptr())
+
+    @classmethod
+    def empty(cls, rows: int, cols: int, layout: int = MX4_ROWS, device="cuda"):
+        import torch
+        n = _lib.ngram_mx4_scale_bytes(int(rows), int(cols), int(layout))
+        return cls(torch.empty((rows, cols // 2), dtype=torch.uint8, device=device),
+                   torch.empty((rows, cols // 32) if layout == MX4_ROWS else n, dtype=torch.uint8, device=device),
+                   rows, cols, layout)
+
+    def need(self, layout, what):
+        if self.layout != layout:
+            raise NgramError(f"{what} needs its scales {'in tiles' if layout == MX4_TILES else 'by rows'}")
+        return self
+
+
+def ngram_mx4_quantize(x, out: Mx4, stream=None):
+    """Quantise the rows of x (bf16 or f32 [rows, cols], rows may be strided) into `out`."""
+    code = _rows2d(x, "x", out.codes.device)
+    if tuple(x.shape) != (out.rows, out.cols):
+        raise NgramError(f"x is {tuple(x.shape)}, out {(out.rows, out.cols)}")
+    rc = _lib.ngram_mx4_quantize(_ptr(x), code, out.rows, out.cols, _stride(x), _ptr(out.codes), _ptr(out.scales),
+                                 out.layout, _device_stream(stream, x))
+    _check(rc, "ngram_mx4_quantize")
+
+
+def new_mx4_workspace(M: int, N: int, K: int, device="cuda"):
+    """A zeroed workspace for products of up to these sizes."""
+    import torch
+    return torch.zeros(_lib.ngram_mx4_product_workspace_bytes(int(M), int(N), int(K)), dtype=torch.uint8, device=device)
+
+
+def ngram_mx4_product(a: Mx4, b: Mx4, out, workspace, alpha: float = 1.0, stream=None):
+    """out = alpha * a b^T for a [M, K] and b [N, K] with scales in tiles (out bf16 or f32)."""
+    a.need(MX4_TILES, "a"), b.need(MX4_TILES, "b")
+    code = _rows2d(out, "out", a.codes.device)
+    _on(out.device, b=b.codes, workspace=workspace)
+    if a.cols != b.cols or tuple(out.shape) != (a.rows, b.rows):
+        raise NgramError(f"shapes do not fit: a {(a.rows, a.cols)}, b {(b.rows, b.cols)}, out {tuple(out.shape)}")
+    rc = _lib.ngram_mx4_product(ctypes.byref(a.struct), ctypes.byref(b.struct), a.rows, b.rows, a.cols, float(alpha),
+                                _ptr(out), code, _stride(out), _ptr(workspace), _bytes_of(workspace),
+                                _device_stream(stream, out))
+    _check(rc, "ngram_mx4_product")
+
+
+def new_embed_mx4_workspace(plan: Plan, max_tokens: int, device="cuda"):
+    """A zeroed workspace for the layer on 4-bit tables; raises for a plan it does not serve."""
+    import torch
+    n = _lib.ngram_embed_mx4_workspace_bytes(plan.handle, int(max_tokens))
+    if n == 0:
+        raise NgramError("the layer on 4-bit tables needs N >= 2 and sub-rows of a multiple of 32")
+    return torch.zeros(n, dtype=torch.uint8, device=device)
+
+
+def _mx4_layer(plan: Plan, tokens, E0, E_nk, W: Mx4, out, workspace):
+    code = _rows2d(out, "out", tokens.device)
+    _rows2d(E0, "E0", tokens.device)
+    if code != plan.dtype or E0.dtype != out.dtype or not out.is_contiguous() or not E0.is_contiguous():
+        raise NgramError("out and E0 must be contiguous and of the plan's dtype")
+    if tuple(out.shape) != (tokens.numel(), plan.D) or tuple(E0.shape) != (plan.V0, plan.D):
+        raise NgramError(f"out must be {(tokens.numel(), plan.D)} and E0 {(plan.V0, plan.D)}")
+    if len(E_nk) != plan.S or any((e.rows, e.cols) != (v, plan.d) for e, v in zip(E_nk, plan.V_nk)):
+        raise NgramError(f"E_nk must hold {plan.S} tables [V_nk, {plan.d}]")
+    if (W.rows, W.cols) != (plan.D, plan.D):
+        raise NgramError(f"W must be {(plan.D, plan.D)}")
+    W.need(MX4_TILES, "W")
+    _on(tokens.device, W=W.codes, workspace=workspace, **{f"E_nk[{s}]": e.need(MX4_ROWS, "E_nk").codes
+                                                         for s, e in enumerate(E_nk)})
+    return (_Mx4 * max(plan.S, 1))(*[e.struct for e in E_nk])
+
+
+def ngram_embed_fwd_mx4(plan: Plan, tokens, seq_offsets, E0, E_nk, W: Mx4, out, workspace, cache: Cache | None = None,
+                        cache_slots=None, stream=None):
+    """The layer from 4-bit sub-tables (Mx4 by rows) and a 4-bit W_stacked (Mx4 in tiles)."""
+    _ids(tokens, "tokens"), _ids(seq_offsets, "seq_offsets")
+    tabs = _mx4_layer(plan, tokens, E0, E_nk, W, out, workspace)
+    if cache_slots is not None:
+        _ids(cache_slots, "cache_slots", seq_offsets.numel() - 1)
+    rc = _lib.ngram_embed_fwd_mx4(plan.handle, _ptr(tokens), _ptr(seq_offsets), seq_offsets.numel() - 1, tokens.numel(),
+                                  _ptr(E0), tabs, ctypes.byref(W.struct), ctypes.byref(cache.struct) if cache else None,
+                                  _ptr(cache_slots), _ptr(out), _ptr(workspace), _bytes_of(workspace),
+                                  _device_stream(stream, out))
+    _check(rc, "ngram_embed_fwd_mx4")
+
+
+def ngram_embed_project_mx4(plan: Plan, tokens, idx, E0, E_nk, W: Mx4, out, workspace, stream=None):
+    """That layer's projection, given the indices of ngram_hash_indices."""
+    _ids(tokens, "tokens"), _ids(idx, "idx", tokens.numel() * plan.S)
+    tabs = _mx4_layer(plan, tokens, E0, E_nk, W, out, workspace)
+    rc = _lib.ngram_embed_project_mx4(plan.handle, _ptr(tokens), _ptr(idx), tokens.numel(), _ptr(E0), tabs,
+                                      ctypes.byref(W.struct), _ptr(out), _ptr(workspace), _bytes_of(workspace),
+                                      _device_stream(stream, out))
+    _check(rc, "ngram_embed_project_mx4")
+
+
+def new_embedding_workspace(max_ids: int, D: int, device="cuda"):
+    """A zeroed workspace for a table's lookup (any max_ids) and its gradient (up to max_ids)."""
+    import torch
+    return torch.zeros(_lib.ngram_embedding_workspace_bytes(int(max_ids), int(D)), dtype=torch.uint8, device=device)
+
+
+def ngram_embedding_fwd(table, ids, out, workspace, scale: float = 1.0, pad_id: int = -1, stream=None):
+    """out[i] = scale * table[ids[i]]; ids None: the table's first rows in order. The table is a
+    contiguous bf16 or f32 matrix, or an Mx4 by rows; positions of pad_id get zeros."""
+    out_code = _rows2d(out, "out")
+    if isinstance(table, Mx4):
+        table.need(MX4_ROWS, "table")
+        base, scales, code, V, D = table.codes, table.scales, NGRAM_MX4, table.rows, table.cols
+    else:
+        code = _rows2d(table, "table")
+        if not table.is_contiguous():
+            raise NgramError("table must be contiguous")
+        base, scales, V, D = table, None, table.shape[0], table.shape[1]
+    _on(out.device, table=base, workspace=workspace, ids=ids)
+    if out.shape[1] != D:
+        raise NgramError(f"out has {out.shape[1]} columns, the table {D}")
+    rc = _lib.ngram_embedding_fwd(_ptr(base), _ptr(scales), code, V, D,
+                                  None if ids is None else _ids(ids, "ids", out.shape[0]), out.shape[0], float(scale),
+                                  int(pad_id), _ptr(out), out_code, _stride(out), _ptr(workspace), _bytes_of(workspace),
+                                  _device_stream(stream, out))
+    _check(rc, "ngram_embedding_fwd")
+
+
+def _f32_dense(t, name):
+    import torch
+    if t.dtype != torch.float32 or not t.is_cuda or not t.is_contiguous() or t.dim() != 2:
+        raise NgramError(f"{name} must be a contiguous f32 CUDA matrix")
+    return _ptr(t)
+
+
+def ngram_embedding_bwd(ids, grad_out, d_table, workspace, scale: float = 1.0, pad_id: int = -1, stream=None):
+    """d_table [V, D] (f32) += the lookup's gradient for grad_out [n, D] (bf16 or f32)."""
+    code = _rows2d(grad_out, "grad_out")
+    dt = _f32_dense(d_table, "d_table")
+    _on(grad_out.device, ids=ids, d_table=d_table, workspace=workspace)
+    if d_table.shape[1] != grad_out.shape[1]:
+        raise NgramError(f"d_table has {d_table.shape[1]} columns, grad_out {grad_out.shape[1]}")
+    n, D = grad_out.shape
+    rc = _lib.ngram_embedding_bwd(_ids(ids, "ids", n), n, _ptr(grad_out), code, _stride(grad_out), d_table.shape[0], D,
+                                  float(scale), int(pad_id), dt, _ptr(workspace), _bytes_of(workspace),
+                                  _device_stream(stream, grad_out))
+    _check(rc, "ngram_embedding_bwd")
+
+
+def ngram_embedding_bwd_rows(ids, grad_out, V: int, rows, num_rows, grads, workspace, scale: float = 1.0,
+                             pad_id: int = -1, stream=None):
+    """The same gradient as rows: the distinct ids ascending in rows[:num_rows], their sums in
+    grads[:num_rows] (f32); both hold room for n rows, num_rows is one int32 on the device."""
+    code = _rows2d(grad_out, "grad_out")
+    gr = _f32_dense(grads, "grads")
+    _on(grad_out.device, ids=ids, rows=rows, num_rows=num_rows, grads=grads, workspace=workspace)
+    n, D = grad_out.shape
+    if grads.shape[0] < n or grads.shape[1] != D or rows.numel() < n:
+        raise NgramError(f"rows and grads need room for {n} rows of {D}")
+    rc = _lib.ngram_embedding_bwd_rows(_ids(ids, "ids", n), n, _ptr(grad_out), code, _stride(grad_out), int(V), D,
+                                       float(scale), int(pad_id), _ids(rows, "rows"), _ids(num_rows, "num_rows", 1), gr,
+                                       _ptr(workspace), _bytes_of(workspace), _device_stream(stream, grad_out))
+    _check(rc, "ngram_embedding_bwd_rows")

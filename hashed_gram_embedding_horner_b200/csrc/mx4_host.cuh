@@ -1,0 +1,506 @@
+// Host side of the 4-bit table operators and of the table lookup with its gradient
+// (included by ngram_embed.cu after its own helpers).
+#pragma once
+
+namespace {
+
+// Makes the device that owns `p` current for a call, and the caller's again after it. Calls
+// without a plan take their device from a pointer; host memory is refused there.
+struct DeviceScope {
+  int prev = -1;
+  bool changed = false;
+  int rc = NGRAM_OK;
+  explicit DeviceScope(const void* p) {
+    cudaPointerAttributes a{};
+    if (cudaGetDevice(&prev) != cudaSuccess || cudaPointerGetAttributes(&a, p) != cudaSuccess) {
+      (void)cudaGetLastError();
+      rc = NGRAM_ERR_CUDA;
+      return;
+    }
+    if (a.type != cudaMemoryTypeDevice && a.type != cudaMemoryTypeManaged) {
+      rc = NGRAM_ERR_INVALID_ARG;
+      return;
+    }
+    enter(a.device);
+  }
+  explicit DeviceScope(const ngram_embed_plan* plan) {
+    if (plan->device < 0 || cudaGetDevice(&prev) != cudaSuccess) {
+      rc = NGRAM_ERR_CUDA;
+      return;
+    }
+    enter(plan->device);
+  }
+  void enter(int dev) {
+    if (dev == prev) return;
+    if (cudaSetDevice(dev) != cudaSuccess) rc = NGRAM_ERR_CUDA;
+    else changed = true;
+  }
+  ~DeviceScope() {
+    if (changed) cudaSetDevice(prev);
+  }
+  DeviceScope(const DeviceScope&) = delete;
+  DeviceScope& operator=(const DeviceScope&) = delete;
+};
+
+int device_sms() {
+  int dev = -1, sms = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess ||
+      cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
+    return 0;
+  return sms;
+}
+
+size_t mx4_tiled_scale_bytes(int64_t rows, int64_t cols) {
+  return static_cast<size_t>((rows + 127) / 128) * static_cast<size_t>((cols + 127) / 128) * kMxTileBytes;
+}
+
+// 2-D map over 4-bit codes: boxes of one 128-byte swizzle row (256 elements) x box_rows. Rows
+// and bytes outside the array read zero codes.
+int encode_codes(CUtensorMap* m, const void* base, int64_t cols, int64_t rows, int box_rows) {
+  auto fn = encode_fn();
+  if (!fn) return NGRAM_ERR_CUDA;
+  const cuuint64_t dims[2] = {static_cast<cuuint64_t>(cols / 2), static_cast<cuuint64_t>(rows)};
+  const cuuint64_t strides[1] = {static_cast<cuuint64_t>(cols / 2)};
+  const cuuint32_t box[2] = {128, static_cast<cuuint32_t>(box_rows)};
+  const cuuint32_t estr[2] = {1, 1};
+  const CUresult r = fn(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void*>(base), dims, strides, box, estr,
+                        CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                        CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return r == CUDA_SUCCESS ? NGRAM_OK : NGRAM_ERR_CUDA;
+}
+
+template <int BN, int STAGES, typename OutT>
+int launch_mx4_tiles(Mx4GemmParams prm, const uint8_t* A, const uint8_t* B, int sms, cudaStream_t st) {
+  using L = Mx4Smem<BN, STAGES>;
+  static_assert(L::kLaunchBytes <= 232448, "4-bit product stages exceed 227 KB of shared memory");
+  auto kern = mx4_gemm_kernel<BN, STAGES, OutT>;
+  if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, L::kLaunchBytes) != cudaSuccess)
+    return NGRAM_ERR_CUDA;
+  Mx4Maps maps;
+  int rc = encode_codes(&maps.A, A, prm.K, prm.M, 128);
+  if (rc) return rc;
+  if ((rc = encode_codes(&maps.B, B, prm.K, prm.N, BN))) return rc;
+  prm.num_m_blocks = (prm.M + 127) / 128;
+  prm.num_n_blocks = (prm.N + BN - 1) / BN;
+  const int64_t tiles = static_cast<int64_t>(prm.num_m_blocks) * prm.num_n_blocks;
+  if (tiles > INT32_MAX / 2) return NGRAM_ERR_UNSUPPORTED;
+  const int grid = tiles < sms ? static_cast<int>(tiles) : sms;
+  return launch(kern, dim3(static_cast<unsigned>(grid)), dim3(kMxThreads), L::kLaunchBytes, st, false, 1, maps, prm);
+}
+
+template <typename OutT>
+int launch_mx4_gemm(Mx4GemmParams prm, const uint8_t* A, const uint8_t* B, int sms, cudaStream_t st) {
+  if (sms < 1) return NGRAM_ERR_CUDA;
+  prm.kt = (prm.K + 127) / 128;
+  prm.num_k_blocks = (prm.K + 255) / 256;
+  // the width whose waves of tiles bring in the fewest bytes an SM: (128 + BN) rows a tile
+  auto cost = [&](int bn) {
+    const int64_t tiles = static_cast<int64_t>((prm.M + 127) / 128) * ((prm.N + bn - 1) / bn);
+    return (tiles + sms - 1) / sms * (128 + bn);
+  };
+  if (cost(256) <= cost(128) && cost(256) <= cost(64)) return launch_mx4_tiles<256, 4, OutT>(prm, A, B, sms, st);
+  if (cost(128) <= cost(64)) return launch_mx4_tiles<128, 6, OutT>(prm, A, B, sms, st);
+  return launch_mx4_tiles<64, 7, OutT>(prm, A, B, sms, st);
+}
+
+// Workspace of the layer on 4-bit tables: [head | T x S indices | T x D / 2 codes | scale tiles]
+struct Mx4LayerWs {
+  int32_t* idx;
+  uint8_t *G, *Gs;
+  size_t bytes;
+};
+Mx4LayerWs mx4_layer_ws(const ngram_embed_plan* p, int64_t T, void* ws) {
+  Mx4LayerWs w{};
+  const size_t at_g = ws_base(p, T);
+  const size_t at_s = at_g + round256(static_cast<size_t>(T) * static_cast<size_t>(p->D) / 2);
+  w.bytes = at_s + round256(mx4_tiled_scale_bytes(T, p->D));
+  if (ws) {
+    auto* b = static_cast<uint8_t*>(ws);
+    w.idx = idx_ptr(ws);
+    w.G = b + at_g;
+    w.Gs = b + at_s;
+  }
+  return w;
+}
+
+bool mx4_plan_ok(const ngram_embed_plan* p) { return p->S > 0 && p->d % kMxBlock == 0; }
+
+int check_mx4_layer(const ngram_embed_plan* p, const int32_t* tokens, const void* E0, const ngram_mx4* E_nk,
+                    const ngram_mx4* W, void* out) {
+  if (!tokens || !E0 || !E_nk || !W || !W->codes || !W->scales || !out) return NGRAM_ERR_INVALID_ARG;
+  if (!aligned16(E0) || !aligned16(out) || !aligned16(W->codes) || !aligned16(W->scales)) return NGRAM_ERR_MISALIGNED;
+  for (int s = 0; s < p->S; ++s) {
+    if (!E_nk[s].codes || !E_nk[s].scales) return NGRAM_ERR_INVALID_ARG;
+    if (!aligned16(E_nk[s].codes)) return NGRAM_ERR_MISALIGNED;
+  }
+  return NGRAM_OK;
+}
+
+int project_mx4(const ngram_embed_plan* p, const int32_t* tokens, const int32_t* idx, int64_t T, const void* E0,
+                const ngram_mx4* E_nk, const ngram_mx4* W, void* out, const Mx4LayerWs& w, void* ws, cudaStream_t st) {
+  Mx4GatherParams g{};
+  for (int s = 0; s < p->S; ++s) {
+    g.E[s].codes = static_cast<const uint8_t*>(E_nk[s].codes);
+    g.E[s].scales = static_cast<const uint8_t*>(E_nk[s].scales);
+    g.Vs[s] = static_cast<uint32_t>(p->V[s]);
+  }
+  g.idx = idx;
+  g.tokens = tokens;
+  g.V0 = static_cast<uint32_t>(p->V0);
+  g.T = static_cast<uint32_t>(T);
+  g.S = p->S;
+  g.row_blocks = p->d / kMxBlock;
+  g.kt = (p->D + 127) / 128;
+  g.by_row.set(static_cast<uint32_t>(g.kt) * 4);
+  g.by_sub.set(static_cast<uint32_t>(g.row_blocks));
+  g.blocks = p->D / kMxBlock;
+  g.G = w.G;
+  g.Gs = w.Gs;
+  g.status = status_ptr(ws);
+  const int64_t vecs = T * g.kt * 4;
+  constexpr int64_t per_block = 256 * kMx4GatherUnroll;
+  if (vecs + per_block > UINT32_MAX) return NGRAM_ERR_UNSUPPORTED;  // numbered in 32 bits
+  int rc = launch(mx4_gather_kernel, dim3(static_cast<unsigned>((vecs + per_block - 1) / per_block)), dim3(256), 0, st,
+                  p->pdl, 1, g);
+  if (rc) return rc;
+  Mx4GemmParams prm{};
+  prm.sa = w.Gs;
+  prm.sb = static_cast<const uint8_t*>(W->scales);
+  prm.M = static_cast<int>(T);
+  prm.N = p->D;
+  prm.K = p->D;
+  prm.scale = p->out_scale / static_cast<float>(p->S + 1);
+  prm.tokens = tokens;
+  prm.E0 = E0;
+  prm.V0 = static_cast<uint32_t>(p->V0);
+  prm.out = out;
+  prm.ldo = p->D;
+  prm.vec = 1;  // D * element size is a multiple of 16, as out's address
+  prm.status = status_ptr(ws);
+  const auto* Wc = static_cast<const uint8_t*>(W->codes);
+  return p->dtype == NGRAM_F32 ? launch_mx4_gemm<float>(prm, w.G, Wc, p->sms, st)
+                               : launch_mx4_gemm<uint16_t>(prm, w.G, Wc, p->sms, st);
+}
+
+// ---- lookup and gradient of one table ----
+struct GradWs {
+  uint32_t *key[2], *counts, *totals, *tile_heads;
+  int32_t *pos[2], *piece_run;
+  float* partial;
+  size_t bytes;
+};
+GradWs grad_ws(int64_t n, int64_t D, void* ws) {
+  GradWs w{};
+  size_t off = kHeadBytes;
+  auto take = [&](size_t b) {
+    const size_t at = off;
+    off += round256(b);
+    return at;
+  };
+  const size_t N = static_cast<size_t>(n);
+  const size_t tiles = (N + kSortTile - 1) / kSortTile, pieces = (N + kGradPiece - 1) / kGradPiece;
+  const size_t k0 = take(N * 4), k1 = take(N * 4), p0 = take(N * 4), p1 = take(N * 4);
+  const size_t cn = take(tiles << (kSortMaxBits + 2)), to = take(4u << kSortMaxBits), th = take(tiles * 4);
+  const size_t pr = take(pieces * 4), pa = take(pieces * 2 * static_cast<size_t>(D) * 4);
+  w.bytes = off;
+  if (ws) {
+    auto* b = static_cast<uint8_t*>(ws);
+    w.key[0] = reinterpret_cast<uint32_t*>(b + k0);
+    w.key[1] = reinterpret_cast<uint32_t*>(b + k1);
+    w.pos[0] = reinterpret_cast<int32_t*>(b + p0);
+    w.pos[1] = reinterpret_cast<int32_t*>(b + p1);
+    w.counts = reinterpret_cast<uint32_t*>(b + cn);
+    w.totals = reinterpret_cast<uint32_t*>(b + to);
+    w.tile_heads = reinterpret_cast<uint32_t*>(b + th);
+    w.piece_run = reinterpret_cast<int32_t*>(b + pr);
+    w.partial = reinterpret_cast<float*>(b + pa);
+  }
+  return w;
+}
+
+int embedding_bwd(const int32_t* ids, int64_t n, const void* g, int g_dtype, int64_t g_stride, int64_t V, int64_t D,
+                  float scale, int64_t pad_id, int32_t* rows_out, int32_t* count_out, float* out, bool dense,
+                  void* workspace, size_t workspace_bytes, void* stream) {
+  if (n < 0 || n > INT32_MAX || V < 1 || V >= (int64_t(1) << 31) || D < 1 || D > INT32_MAX || !(scale - scale == 0.0f) ||
+      (g_dtype != NGRAM_BF16 && g_dtype != NGRAM_F32) || !workspace || (!dense && !count_out) ||
+      (n > 0 && (!ids || !g || !out || (!dense && !rows_out) || g_stride < D)))
+    return NGRAM_ERR_INVALID_ARG;
+  if (D % 8 != 0) return NGRAM_ERR_UNSUPPORTED;
+  const int elt = g_dtype == NGRAM_BF16 ? 2 : 4;
+  if (!aligned16(workspace)) return NGRAM_ERR_MISALIGNED;
+  if (n > 0 && (!aligned16(g) || !aligned16(out) || g_stride * elt % 16 != 0)) return NGRAM_ERR_MISALIGNED;
+  const GradWs w = grad_ws(n, D, workspace);
+  if (workspace_bytes < w.bytes) return NGRAM_ERR_WORKSPACE;
+  const DeviceScope dev(workspace);
+  if (dev.rc) return dev.rc;
+  const cudaStream_t st = static_cast<cudaStream_t>(stream);
+  if (n == 0) {
+    if (!dense && cudaMemsetAsync(count_out, 0, 4, st) != cudaSuccess) return NGRAM_ERR_CUDA;
+    return NGRAM_OK;
+  }
+  // keys 0 .. V (V: a padded position), in equal digits of at most kSortMaxBits bits
+  int bits = 1;
+  while ((V >> bits) != 0) ++bits;
+  const int passes = (bits + kSortMaxBits - 1) / kSortMaxBits;
+  SortParams s{};
+  s.ids = ids;
+  s.V = static_cast<uint32_t>(V);
+  s.pad_id = pad_id;
+  s.n = static_cast<uint32_t>(n);
+  s.bits = (bits + passes - 1) / passes;
+  s.tiles = static_cast<uint32_t>((n + kSortTile - 1) / kSortTile);
+  s.counts = w.counts;
+  s.totals = w.totals;
+  s.status = status_ptr(workspace);
+  int rc, cur = 0;
+  for (int k = 0; k < passes; ++k) {
+    s.shift = k * s.bits;
+    s.key_in = k ? w.key[cur ^ 1] : nullptr;
+    s.pos_in = k ? w.pos[cur ^ 1] : nullptr;
+    s.key_out = w.key[cur];
+    s.pos_out = w.pos[cur];
+    if ((rc = launch(sort_count_kernel, dim3(s.tiles), dim3(kSortThreads), 0, st, false, 1, s))) return rc;
+    if ((rc = launch(sort_scan_kernel, dim3(1u << s.bits), dim3(kSortThreads), 0, st, false, 1, s))) return rc;
+    if ((rc = launch(sort_scatter_kernel, dim3(s.tiles), dim3(kSortThreads), 0, st, false, 1, s))) return rc;
+    cur ^= 1;
+  }
+  GradParams r{};
+  r.key = w.key[cur ^ 1];
+  r.pos = w.pos[cur ^ 1];
+  r.n = s.n;
+  r.V = s.V;
+  r.tiles = s.tiles;
+  r.tile_heads = w.tile_heads;
+  r.piece_run = w.piece_run;
+  r.rows_out = rows_out;
+  r.count_out = count_out;
+  r.g = g;
+  r.g_stride = g_stride;
+  r.D = static_cast<int>(D);
+  r.chunks = static_cast<int>((D + 255) / 256);
+  r.scale = scale;
+  r.partial = w.partial;
+  r.out = out;
+  r.dense = dense ? 1 : 0;
+  if ((rc = launch(grad_heads_kernel, dim3(r.tiles), dim3(kSortThreads), 0, st, false, 1, r))) return rc;
+  if ((rc = launch(grad_number_kernel, dim3(r.tiles), dim3(kSortThreads), 0, st, false, 1, r))) return rc;
+  const int64_t items = (n + kGradPiece - 1) / kGradPiece * r.chunks;
+  if (items > int64_t(INT32_MAX) * 8) return NGRAM_ERR_UNSUPPORTED;
+  const dim3 grid(static_cast<unsigned>((items + 7) / 8));
+  rc = g_dtype == NGRAM_BF16 ? launch(grad_reduce_kernel<uint16_t>, grid, dim3(256), 0, st, false, 1, r)
+                             : launch(grad_reduce_kernel<float>, grid, dim3(256), 0, st, false, 1, r);
+  if (rc) return rc;
+  return launch(grad_join_kernel, grid, dim3(256), 0, st, false, 1, r);
+}
+
+template <int TABLE>
+int launch_lookup(const LookupParams& p, int out_dtype, cudaStream_t st) {
+  constexpr uint32_t per_block = 256 * kLookupUnroll;
+  const dim3 grid((p.vecs + per_block - 1) / per_block);
+  return out_dtype == NGRAM_BF16 ? launch(lookup_kernel<TABLE, uint16_t>, grid, dim3(256), 0, st, false, 1, p)
+                                 : launch(lookup_kernel<TABLE, float>, grid, dim3(256), 0, st, false, 1, p);
+}
+
+// Rows a launch numbers in 32 bits: at most 2^30 vectors of eight elements.
+int64_t rows_per_launch(int64_t cols) {
+  const int64_t r = (int64_t(1) << 30) / (cols / 8);
+  return r < 1 ? 1 : r;
+}
+
+}  // namespace
+
+extern "C" {
+
+size_t ngram_mx4_scale_bytes(int64_t rows, int64_t cols, int layout) {
+  if (rows < 0 || cols < 1 || cols % kMxBlock != 0 || (layout != NGRAM_MX4_ROWS && layout != NGRAM_MX4_TILES)) return 0;
+  return layout == NGRAM_MX4_ROWS ? static_cast<size_t>(rows) * static_cast<size_t>(cols / kMxBlock)
+                                  : mx4_tiled_scale_bytes(rows, cols);
+}
+
+int ngram_mx4_quantize(const void* src, int dtype, int64_t rows, int64_t cols, int64_t src_stride, void* codes,
+                       void* scales, int layout, void* stream) {
+  if (rows < 0 || rows > INT32_MAX || cols < 1 || cols > INT32_MAX || (dtype != NGRAM_BF16 && dtype != NGRAM_F32) ||
+      (layout != NGRAM_MX4_ROWS && layout != NGRAM_MX4_TILES) ||
+      (rows > 0 && (!src || !codes || !scales || src_stride < cols)))
+    return NGRAM_ERR_INVALID_ARG;
+  if (cols % kMxBlock != 0) return NGRAM_ERR_UNSUPPORTED;
+  if (rows == 0) return NGRAM_OK;
+  const int elt = dtype == NGRAM_BF16 ? 2 : 4;
+  if (!aligned16(codes) || !aligned16(scales) || reinterpret_cast<uintptr_t>(src) % elt != 0) return NGRAM_ERR_MISALIGNED;
+  const DeviceScope dev(codes);
+  if (dev.rc) return dev.rc;
+  const bool vec = aligned16(src) && src_stride * elt % 16 == 0;
+  const int64_t step = rows_per_launch(cols);
+  for (int64_t r0 = 0; r0 < rows; r0 += step) {
+    const int64_t r = rows - r0 < step ? rows - r0 : step;
+    Mx4QuantParams p{};
+    p.src = static_cast<const uint8_t*>(src) + r0 * src_stride * elt;
+    p.src_stride = src_stride;
+    p.vecs = static_cast<uint32_t>(r * (cols / 8));
+    p.per_row.set(static_cast<uint32_t>(cols / 8));
+    p.row0 = r0;
+    p.cols = static_cast<int>(cols);
+    p.kt = static_cast<int>((cols + 127) / 128);
+    p.codes = static_cast<uint8_t*>(codes) + r0 * (cols / 2);
+    p.tiles = layout == NGRAM_MX4_TILES ? 1 : 0;
+    p.scales = static_cast<uint8_t*>(scales) + (p.tiles ? 0 : r0 * (cols / kMxBlock));
+    constexpr uint32_t per_block = 256 * kMx4QuantUnroll;
+    const dim3 grid((p.vecs + per_block - 1) / per_block);
+    const cudaStream_t st = static_cast<cudaStream_t>(stream);
+    int rc;
+    if (dtype == NGRAM_BF16)
+      rc = vec ? launch(mx4_quantize_kernel<uint16_t, true>, grid, dim3(256), 0, st, false, 1, p)
+               : launch(mx4_quantize_kernel<uint16_t, false>, grid, dim3(256), 0, st, false, 1, p);
+    else
+      rc = vec ? launch(mx4_quantize_kernel<float, true>, grid, dim3(256), 0, st, false, 1, p)
+               : launch(mx4_quantize_kernel<float, false>, grid, dim3(256), 0, st, false, 1, p);
+    if (rc) return rc;
+  }
+  return NGRAM_OK;
+}
+
+size_t ngram_mx4_product_workspace_bytes(int64_t M, int64_t N, int64_t K) {
+  if (M < 0 || N < 0 || K < 1) return 0;
+  return kHeadBytes;
+}
+
+int ngram_mx4_product(const ngram_mx4* A, const ngram_mx4* B, int64_t M, int64_t N, int64_t K, float alpha, void* out,
+                      int out_dtype, int64_t out_stride, void* workspace, size_t workspace_bytes, void* stream) {
+  if (!A || !B || M < 0 || M > INT32_MAX - 256 || N < 0 || N > INT32_MAX - 256 || K < 1 || K > INT32_MAX - 256 ||
+      !(alpha - alpha == 0.0f) || (out_dtype != NGRAM_BF16 && out_dtype != NGRAM_F32) || !workspace ||
+      out_stride < N)
+    return NGRAM_ERR_INVALID_ARG;
+  if (K % kMxBlock != 0) return NGRAM_ERR_UNSUPPORTED;
+  if (!aligned16(workspace)) return NGRAM_ERR_MISALIGNED;
+  if (workspace_bytes < ngram_mx4_product_workspace_bytes(M, N, K)) return NGRAM_ERR_WORKSPACE;
+  if (M == 0 || N == 0) return NGRAM_OK;
+  if (!A->codes || !A->scales || !B->codes || !B->scales || !out) return NGRAM_ERR_INVALID_ARG;
+  const int elt = out_dtype == NGRAM_BF16 ? 2 : 4;
+  if (!aligned16(A->codes) || !aligned16(A->scales) || !aligned16(B->codes) || !aligned16(B->scales) ||
+      reinterpret_cast<uintptr_t>(out) % elt != 0)
+    return NGRAM_ERR_MISALIGNED;
+  const DeviceScope dev(workspace);
+  if (dev.rc) return dev.rc;
+  Mx4GemmParams prm{};
+  prm.sa = static_cast<const uint8_t*>(A->scales);
+  prm.sb = static_cast<const uint8_t*>(B->scales);
+  prm.M = static_cast<int>(M);
+  prm.N = static_cast<int>(N);
+  prm.K = static_cast<int>(K);
+  prm.scale = alpha;
+  prm.out = out;
+  prm.ldo = out_stride;
+  prm.vec = aligned16(out) && out_stride * elt % 16 == 0 ? 1 : 0;
+  prm.status = status_ptr(workspace);
+  const auto *Ac = static_cast<const uint8_t*>(A->codes), *Bc = static_cast<const uint8_t*>(B->codes);
+  const cudaStream_t st = static_cast<cudaStream_t>(stream);
+  return out_dtype == NGRAM_F32 ? launch_mx4_gemm<float>(prm, Ac, Bc, device_sms(), st)
+                                : launch_mx4_gemm<uint16_t>(prm, Ac, Bc, device_sms(), st);
+}
+
+size_t ngram_embed_mx4_workspace_bytes(const ngram_embed_plan* plan, int64_t max_tokens) {
+  if (!plan || max_tokens < 0 || !mx4_plan_ok(plan)) return 0;
+  return mx4_layer_ws(plan, max_tokens, nullptr).bytes;
+}
+
+int ngram_embed_project_mx4(const ngram_embed_plan* plan, const int32_t* tokens, const int32_t* idx, int64_t num_tokens,
+                            const void* E0, const ngram_mx4* E_nk, const ngram_mx4* W, void* out, void* workspace,
+                            size_t workspace_bytes, void* stream) {
+  if (!plan || !workspace || num_tokens < 0 || num_tokens > INT32_MAX - 256) return NGRAM_ERR_INVALID_ARG;
+  if (!mx4_plan_ok(plan)) return NGRAM_ERR_UNSUPPORTED;
+  if (!aligned16(workspace)) return NGRAM_ERR_MISALIGNED;
+  const Mx4LayerWs w = mx4_layer_ws(plan, num_tokens, workspace);
+  if (workspace_bytes < w.bytes) return NGRAM_ERR_WORKSPACE;
+  if (num_tokens == 0) return NGRAM_OK;
+  if (!idx) return NGRAM_ERR_INVALID_ARG;
+  int rc = check_mx4_layer(plan, tokens, E0, E_nk, W, out);
+  if (rc) return rc;
+  const DeviceScope dev(plan);
+  if (dev.rc) return dev.rc;
+  return project_mx4(plan, tokens, idx, num_tokens, E0, E_nk, W, out, w, workspace, static_cast<cudaStream_t>(stream));
+}
+
+int ngram_embed_fwd_mx4(const ngram_embed_plan* plan, const int32_t* tokens, const int32_t* seq_offsets,
+                        int32_t num_seqs, int64_t num_tokens, const void* E0, const ngram_mx4* E_nk, const ngram_mx4* W,
+                        const ngram_cache* cache, const int32_t* cache_slots, void* out, void* workspace,
+                        size_t workspace_bytes, void* stream) {
+  if (!plan || !workspace || num_tokens < 0 || num_tokens > INT32_MAX - 256 || num_seqs < 0) return NGRAM_ERR_INVALID_ARG;
+  if (!mx4_plan_ok(plan)) return NGRAM_ERR_UNSUPPORTED;
+  if (!aligned16(workspace)) return NGRAM_ERR_MISALIGNED;
+  const Mx4LayerWs w = mx4_layer_ws(plan, num_tokens, workspace);
+  if (workspace_bytes < w.bytes) return NGRAM_ERR_WORKSPACE;
+  if (num_tokens == 0) return NGRAM_OK;
+  if (!seq_offsets || num_seqs == 0) return NGRAM_ERR_INVALID_ARG;
+  int rc = check_mx4_layer(plan, tokens, E0, E_nk, W, out);
+  if (rc) return rc;
+  if (cache && (rc = validate_cache(plan, cache))) return rc;
+  const DeviceScope dev(plan);
+  if (dev.rc) return dev.rc;
+  const cudaStream_t st = static_cast<cudaStream_t>(stream);
+  if ((rc = launch_hash(plan, tokens, seq_offsets, num_seqs, num_tokens, cache, cache_slots, w.idx, workspace, st)))
+    return rc;
+  return project_mx4(plan, tokens, w.idx, num_tokens, E0, E_nk, W, out, w, workspace, st);
+}
+
+size_t ngram_embedding_workspace_bytes(int64_t max_ids, int64_t D) {
+  if (max_ids < 0 || max_ids > INT32_MAX || D < 1 || D > INT32_MAX) return 0;
+  return grad_ws(max_ids, D, nullptr).bytes;
+}
+
+int ngram_embedding_fwd(const void* table, const void* table_scales, int table_dtype, int64_t V, int64_t D,
+                        const int32_t* ids, int64_t n, float scale, int64_t pad_id, void* out, int out_dtype,
+                        int64_t out_stride, void* workspace, size_t workspace_bytes, void* stream) {
+  if (n < 0 || n > INT32_MAX || V < 1 || V >= (int64_t(1) << 31) || D < 1 || D > INT32_MAX || !(scale - scale == 0.0f) ||
+      (table_dtype != NGRAM_BF16 && table_dtype != NGRAM_F32 && table_dtype != NGRAM_MX4) ||
+      (out_dtype != NGRAM_BF16 && out_dtype != NGRAM_F32) || !workspace || (!ids && n > V))
+    return NGRAM_ERR_INVALID_ARG;
+  if (D % (table_dtype == NGRAM_MX4 ? kMxBlock : 8) != 0) return NGRAM_ERR_UNSUPPORTED;
+  if (!aligned16(workspace)) return NGRAM_ERR_MISALIGNED;
+  if (workspace_bytes < kHeadBytes) return NGRAM_ERR_WORKSPACE;
+  if (n == 0) return NGRAM_OK;
+  if (!table || !out || out_stride < D || (table_dtype == NGRAM_MX4 && !table_scales)) return NGRAM_ERR_INVALID_ARG;
+  const int elt = out_dtype == NGRAM_BF16 ? 2 : 4;
+  if (!aligned16(table) || !aligned16(out) || out_stride * elt % 16 != 0) return NGRAM_ERR_MISALIGNED;
+  const DeviceScope dev(workspace);
+  if (dev.rc) return dev.rc;
+  const int64_t step = rows_per_launch(D);
+  for (int64_t r0 = 0; r0 < n; r0 += step) {
+    const int64_t r = n - r0 < step ? n - r0 : step;
+    LookupParams p{};
+    p.table = table;
+    p.scales = static_cast<const uint8_t*>(table_scales);
+    p.ids = ids ? ids + r0 : nullptr;
+    p.V = static_cast<uint32_t>(V);
+    p.pad_id = pad_id;
+    p.per_row.set(static_cast<uint32_t>(D / 8));
+    p.vecs = static_cast<uint32_t>(r * (D / 8));
+    p.scale = scale;
+    p.out = static_cast<uint8_t*>(out) + r0 * out_stride * elt;
+    p.out_stride = out_stride;
+    p.row0 = r0;
+    p.status = status_ptr(workspace);
+    const cudaStream_t st = static_cast<cudaStream_t>(stream);
+    int rc;
+    if (table_dtype == NGRAM_BF16) rc = launch_lookup<kTableBf16>(p, out_dtype, st);
+    else if (table_dtype == NGRAM_F32) rc = launch_lookup<kTableF32>(p, out_dtype, st);
+    else rc = launch_lookup<kTableMx4>(p, out_dtype, st);
+    if (rc) return rc;
+  }
+  return NGRAM_OK;
+}
+
+int ngram_embedding_bwd(const int32_t* ids, int64_t n, const void* grad_out, int grad_dtype, int64_t grad_stride,
+                        int64_t V, int64_t D, float scale, int64_t pad_id, float* d_table, void* workspace,
+                        size_t workspace_bytes, void* stream) {
+  return embedding_bwd(ids, n, grad_out, grad_dtype, grad_stride, V, D, scale, pad_id, nullptr, nullptr, d_table, true,
+                       workspace, workspace_bytes, stream);
+}
+
+int ngram_embedding_bwd_rows(const int32_t* ids, int64_t n, const void* grad_out, int grad_dtype, int64_t grad_stride,
+                             int64_t V, int64_t D, float scale, int64_t pad_id, int32_t* rows, int32_t* num_rows,
+                             float* grads, void* workspace, size_t workspace_bytes, void* stream) {
+  return embedding_bwd(ids, n, grad_out, grad_dtype, grad_stride, V, D, scale, pad_id, rows, num_rows, grads, false,
+                       workspace, workspace_bytes, stream);
+}
+
+}  // extern "C"

@@ -27,6 +27,8 @@
 #include "stats.cuh"
 #include "draft.cuh"
 #include "decode.cuh"
+#include "mx4.cuh"
+#include "embedding.cuh"
 
 using namespace ngram;
 
@@ -1851,3 +1853,5 @@ extern "C" int ngram_embed_fwd_static_ws(const ngram_embed_plan* plan, const int
     return NGRAM_ERR_CUDA;
   return NGRAM_OK;
 }
+
+#include "mx4_host.cuh"

@@ -70,6 +70,11 @@ extern "C" {
 /* ---- element types ---- */
 #define NGRAM_BF16 0
 #define NGRAM_F32 1
+#define NGRAM_MX4 2 /* 4-bit tables of the calls that name it; not a plan's dtype */
+
+/* ---- layouts of the scales of 4-bit arrays (see ngram_mx4) ---- */
+#define NGRAM_MX4_ROWS 0
+#define NGRAM_MX4_TILES 1
 
 /* ---- limits ---- */
 #define NGRAM_MAX_N 8          /* largest n-gram order */
@@ -320,6 +325,104 @@ int ngram_embed_plan_set_output_scale(ngram_embed_plan* plan, float scale);
 int ngram_embed_layernorm(const ngram_embed_plan* plan, const void* x, int64_t num_tokens,
                           const float* gamma, const float* beta, float eps, void* y,
                           void* workspace, size_t workspace_bytes, void* stream);
+
+/* ---- 4-bit tables: microscaled 4-bit floating point ----
+ * The format is MXFP4 of the OCP Microscaling Formats (MX) specification, v1.0. A row of C
+ * elements (C a multiple of 32) holds
+ *   codes   C / 2 bytes of E2M1 elements, element 2j in the low half of byte j; the
+ *           magnitudes are 0, 0.5, 1, 1.5, 2, 3, 4, 6, bit 3 is the sign;
+ *   scales  one E8M0 byte e for each block of 32 elements: 2^(e - 127), 255 is NaN.
+ * Rows of codes are dense. Scales lie in one of two layouts:
+ *   NGRAM_MX4_ROWS   [rows x C / 32], for tables whose rows are looked up;
+ *   NGRAM_MX4_TILES  512 bytes for 128 rows x 4 blocks, for the operands of a product: the
+ *                    byte of row r, block b is at (r % 32) * 16 + (r / 32 % 4) * 4 + b % 4 of
+ *                    tile (r / 128) * ceil(C / 128) + b / 4. Bytes of blocks past the row's end
+ *                    are 0; those of rows past the last are not read into any result.
+ * At 17/32 bytes an element a table takes 0.27 of its bf16 size. */
+typedef struct {
+  const void* codes;  /* device, 16-byte aligned */
+  const void* scales; /* device; 16-byte aligned in tiles */
+} ngram_mx4;
+
+/* Bytes of the scales of [rows x cols] in a layout; 0 on bad arguments. */
+size_t ngram_mx4_scale_bytes(int64_t rows, int64_t cols, int layout);
+
+/* Quantise src [rows x cols] (NGRAM_BF16 or NGRAM_F32, row stride src_stride elements):
+ *   e    = clamp(floor(log2(max |x| of the block)) - 2 + 127, 0, 254), 0 for a block of zeros;
+ *   code = x / 2^(e - 127) rounded to the nearest E2M1 value, ties to even, saturating at 6.
+ * A block that holds an infinity or a NaN becomes NaN: e = 255, codes 0. cols must be a
+ * multiple of 32 (else NGRAM_ERR_UNSUPPORTED). src is read fastest when it is 16-byte aligned
+ * and its rows' stride is a multiple of 16 bytes; element alignment is enough. */
+int ngram_mx4_quantize(const void* src, int dtype, int64_t rows, int64_t cols, int64_t src_stride,
+                       void* codes, void* scales, int layout, void* stream);
+
+/* out[m][n] = alpha * sum_k A[m][k] B[n][k] for A [M x K] and B [N x K] with scales in tiles:
+ * the block-scaled tensor-core product, fp32 sums, rounded once to out_dtype (NGRAM_BF16 or
+ * NGRAM_F32). out has a row stride of out_stride elements (any; 16-byte aligned rows are
+ * written fastest). K must be a multiple of 32.
+ *   workspace  >= ngram_mx4_product_workspace_bytes(M, N, K); its head as for a plan's
+ *              workspace (zeroed once; status word) */
+size_t ngram_mx4_product_workspace_bytes(int64_t M, int64_t N, int64_t K);
+int ngram_mx4_product(const ngram_mx4* A, const ngram_mx4* B, int64_t M, int64_t N, int64_t K,
+                      float alpha, void* out, int out_dtype, int64_t out_stride, void* workspace,
+                      size_t workspace_bytes, void* stream);
+
+/* The whole layer (Eq. 2 + Eq. 3) with 4-bit sub-tables and a 4-bit projection:
+ *   E_nk  HOST array of S tables [V_nk[s] x d], scales by rows
+ *   W     W_stacked [D x D], scales in tiles
+ * E_0 and out keep the plan's dtype; every other argument, the output scale, the N-gram cache
+ * and the status bits are those of ngram_embed_fwd. The result is Eq. 3 on the values that the
+ * 4-bit tables stand for (fp32 sums, one rounding). Needs N >= 2 and d a multiple of 32 (else
+ * NGRAM_ERR_UNSUPPORTED; any plan dtype).
+ *   workspace  >= ngram_embed_mx4_workspace_bytes(plan, num_tokens): head, indices, the
+ *              gathered sub-rows (17/32 bytes an element); 0 for a plan it does not serve */
+size_t ngram_embed_mx4_workspace_bytes(const ngram_embed_plan* plan, int64_t max_tokens);
+int ngram_embed_fwd_mx4(const ngram_embed_plan* plan, const int32_t* tokens,
+                        const int32_t* seq_offsets, int32_t num_seqs, int64_t num_tokens,
+                        const void* E0, const ngram_mx4* E_nk, const ngram_mx4* W,
+                        const ngram_cache* cache, const int32_t* cache_slots, void* out,
+                        void* workspace, size_t workspace_bytes, void* stream);
+
+/* The projection of that layer alone, as ngram_embed_project. */
+int ngram_embed_project_mx4(const ngram_embed_plan* plan, const int32_t* tokens, const int32_t* idx,
+                            int64_t num_tokens, const void* E0, const ngram_mx4* E_nk,
+                            const ngram_mx4* W, void* out, void* workspace, size_t workspace_bytes,
+                            void* stream);
+
+/* ---- one table: lookup and gradient ----
+ * out[i] = scale * table[ids[i]] for n int32 ids (device), in fp32, rounded once to out_dtype.
+ *   table        [V x D] NGRAM_BF16, NGRAM_F32, or NGRAM_MX4 codes with table_scales by rows
+ *                (NULL otherwise); D a multiple of 8 (NGRAM_MX4: of 32)
+ *   ids          NULL: ids[i] = i, n <= V (a whole table read back)
+ *   pad_id       positions whose id is pad_id get a row of zeros and the gradient skips them;
+ *                negative: none
+ *   out          [n x D] NGRAM_BF16 or NGRAM_F32, row stride out_stride elements (rows and base
+ *                16-byte aligned)
+ *   workspace    >= ngram_embedding_workspace_bytes(0, D): the status word's head. An id outside
+ *                [0, V) reads row 0 and sets NGRAM_STATUS_BAD_TOKEN. */
+size_t ngram_embedding_workspace_bytes(int64_t max_ids, int64_t D);
+int ngram_embedding_fwd(const void* table, const void* table_scales, int table_dtype, int64_t V,
+                        int64_t D, const int32_t* ids, int64_t n, float scale, int64_t pad_id,
+                        void* out, int out_dtype, int64_t out_stride, void* workspace,
+                        size_t workspace_bytes, void* stream);
+
+/* Its gradient: d_table[v] += scale * sum of grad_out[i] over the positions i with ids[i] = v
+ * (d_table [V x D] fp32). grad_out is [n x D] NGRAM_BF16 or NGRAM_F32, row stride grad_stride
+ * elements. Positions are sorted by id and summed in fp32 in a fixed order without atomics:
+ * equal inputs give equal bits. For a 4-bit table this is the gradient of its master (the
+ * straight-through estimate). Ids outside [0, V) count as row 0, as in the lookup.
+ *   workspace  >= ngram_embedding_workspace_bytes(n, D) */
+int ngram_embedding_bwd(const int32_t* ids, int64_t n, const void* grad_out, int grad_dtype,
+                        int64_t grad_stride, int64_t V, int64_t D, float scale, int64_t pad_id,
+                        float* d_table, void* workspace, size_t workspace_bytes, void* stream);
+
+/* The same gradient as rows, for tables too large for a dense one: *num_rows (device int32)
+ * distinct ids, ascending, in rows[0 .. *num_rows), their gradients in grads[u] (fp32 [n x D],
+ * written, not added to). Room for n rows; those past *num_rows are left as they were. */
+int ngram_embedding_bwd_rows(const int32_t* ids, int64_t n, const void* grad_out, int grad_dtype,
+                             int64_t grad_stride, int64_t V, int64_t D, float scale, int64_t pad_id,
+                             int32_t* rows, int32_t* num_rows, float* grads, void* workspace,
+                             size_t workspace_bytes, void* stream);
 
 /* Synchronise `stream` and copy the sticky status word to *status_out. */
 int ngram_embed_get_status(const void* workspace, void* stream, int32_t* status_out);

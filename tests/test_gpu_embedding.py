@@ -1,0 +1,259 @@
+"""The lookup of one table and its gradient by sorted ids, on the GPU, against plain 64-bit
+definitions on the host."""
+import numpy as np
+import pytest
+import torch
+
+from tests import mx4_ref as ref
+
+pytestmark = pytest.mark.gpu
+
+BF16, F32 = torch.bfloat16, torch.float32
+HALF = {BF16: ref.BF16_HALF, F32: ref.F32_HALF}
+
+
+@pytest.fixture(scope="module")
+def ne():
+    import hashed_gram_embedding_horner_b200 as m
+    return m
+
+
+def f64(t):
+    return t.double().cpu().numpy()
+
+
+def ids_of(rng, n, V, kind):
+    if kind == "same":
+        return np.full(n, V // 2, np.int32)
+    if kind == "zipf":
+        return np.minimum(rng.zipf(1.3, n) - 1, V - 1).astype(np.int32)
+    if kind == "distinct":
+        return rng.permutation(max(V, n))[:n].astype(np.int32) % V
+    return rng.integers(0, V, n).astype(np.int32)
+
+
+@pytest.mark.parametrize("out_dtype", [BF16, F32])
+@pytest.mark.parametrize("kind,V,D,n", [
+    ("bf16", 1, 8, 1), ("bf16", 100, 136, 33), ("f32", 50, 8, 7), ("f32", 313, 264, 1000), ("mx4", 9, 32, 5),
+    ("mx4", 1000, 96, 700), ("mx4", 77, 2080, 130), ("bf16", 3000, 1024, 2049),
+])
+def test_lookup(ne, kind, V, D, n, out_dtype):
+    rng = np.random.default_rng(V + D + n)
+    if kind == "mx4":
+        codes, scales = ref.random_mx4(rng, V, D, spread=20)
+        scales[0, 0], scales[V - 1, D // 32 - 1] = 0, 254
+        vals = ref.values(codes, scales)
+        table = ne.Mx4(torch.from_numpy(ref.pack(codes)).cuda(), torch.from_numpy(scales).cuda(), V, D, ne.MX4_ROWS)
+    else:
+        table = torch.from_numpy(rng.standard_normal((V, D))).to(BF16 if kind == "bf16" else F32).cuda()
+        vals = f64(table)
+    ids = rng.integers(0, V, n).astype(np.int32)
+    ids[0], ids[-1] = 0, V - 1
+    ws = ne.new_embedding_workspace(0, D)
+    for scale, pad in ((1.0, -1), (0.37, V - 1), (-2.5, 0)):
+        out = torch.full((n, D), 9.0, dtype=out_dtype, device="cuda")
+        ne.ngram_embedding_fwd(table, torch.from_numpy(ids).cuda(), out, ws, scale=scale, pad_id=pad)
+        want = ref.lookup(vals, ids, scale, pad)
+        # one fp32 product, one rounding to the output type; f32 subnormals: half of 2^-149
+        bound = (ref.F32_HALF + (HALF[out_dtype] if out_dtype == BF16 else 0)) * np.abs(want) * 1.01 + 2.0 ** -149
+        if out_dtype == BF16:
+            bound = np.maximum(bound, 2.0 ** -134)  # half of bf16's smallest subnormal
+        # half a step above the largest number and more is an infinity
+        over = np.abs(want) >= (2 - 2.0 ** (-8 if out_dtype == BF16 else -24)) * 2.0 ** 127
+        got = f64(out)
+        assert (got[over] == np.sign(want[over]) * np.inf).all()
+        assert (np.abs(got[~over] - want[~over]) <= bound[~over]).all()
+    assert ne.ngram_embed_get_status(ws) == 0
+
+
+def test_lookup_into_strided_rows_whole_tables_and_bad_ids(ne):
+    rng = np.random.default_rng(2)
+    table = torch.from_numpy(rng.standard_normal((60, 64))).float().cuda()
+    ws = ne.new_embedding_workspace(0, 64)
+    buf = torch.full((50, 200), 5.0, device="cuda")
+    ne.ngram_embedding_fwd(table, None, buf[:, 64:128], ws)  # ids None: rows 0 .. 49
+    assert torch.equal(buf[:, 64:128], table[:50])
+    assert bool((buf[:, :64] == 5.0).all()) and bool((buf[:, 128:] == 5.0).all())
+    out = torch.empty((4, 64), device="cuda")
+    ne.ngram_embedding_fwd(table, torch.tensor([3, 60, -1, 59], dtype=torch.int32, device="cuda"), out, ws)
+    assert torch.equal(out, table[[3, 0, 0, 59]]) and ne.ngram_embed_get_status(ws) == 0x1
+    ne.ngram_embed_clear_status(ws)
+    assert ne.ngram_embed_get_status(ws) == 0
+
+
+def check_rows(ne, ids, g, V, scale, pad, ws=None):
+    n, D = g.shape
+    ws = ne.new_embedding_workspace(n, D) if ws is None else ws
+    rows = torch.full((n,), -5, dtype=torch.int32, device="cuda")
+    count = torch.full((1,), -5, dtype=torch.int32, device="cuda")
+    grads = torch.full((n, D), 4.0, dtype=F32, device="cuda")
+    ids_d = torch.from_numpy(ids).cuda()
+    ne.ngram_embedding_bwd_rows(ids_d, g, V, rows, count, grads, ws, scale=scale, pad_id=pad)
+    want_rows, want, mags, cnt = ref.grad_rows(ids, f64(g), scale, pad)
+    U = int(count)
+    assert U == len(want_rows) and np.array_equal(rows[:U].cpu().numpy(), want_rows)
+    assert (np.abs(f64(grads[:U]) - want) <= ref.grad_bound(mags, cnt)).all()
+    assert bool((rows[U:] == -5).all()) and bool((grads[U:] == 4.0).all())  # left as they were
+    dense = torch.ones((V, D), dtype=F32, device="cuda")
+    ne.ngram_embedding_bwd(ids_d, g, dense, ws, scale=scale, pad_id=pad)
+    full = torch.ones((V, D), dtype=F32, device="cuda")
+    full[rows[:U].long()] += grads[:U]
+    assert torch.equal(dense, full)
+    return rows, grads, U
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("n,V,D,kind", [
+    (1, 1, 8, "same"), (2, 5, 16, "same"), (31, 7, 8, "uniform"), (32, 1000, 40, "distinct"), (33, 3, 264, "uniform"),
+    (64, 40, 256, "same"), (65, 40, 256, "same"), (257, 255, 136, "uniform"), (1024, 256, 24, "zipf"),
+    (1025, 257, 8, "zipf"), (1500, 100000, 512, "distinct"), (3000, 70000, 72, "zipf"), (5000, 1 << 24, 8, "uniform"),
+    (7001, 50, 32, "uniform"), (20000, 131072, 16, "zipf"),
+])
+def test_gradient_rows_and_dense(ne, n, V, D, kind, dtype):
+    rng = np.random.default_rng(n + V)
+    ids = ids_of(rng, n, V, kind)
+    g = torch.from_numpy(rng.standard_normal((n, D))).to(dtype).cuda()
+    if V <= 131072:
+        check_rows(ne, ids, g, V, 1.0, -1)
+        check_rows(ne, ids, g, V, 0.3, int(ids[n // 2]))
+    else:  # a dense table of this many rows is left out
+        ws = ne.new_embedding_workspace(n, D)
+        rows, count = torch.zeros(n, dtype=torch.int32, device="cuda"), torch.zeros(1, dtype=torch.int32, device="cuda")
+        grads = torch.zeros((n, D), device="cuda")
+        ne.ngram_embedding_bwd_rows(torch.from_numpy(ids).cuda(), g, V, rows, count, grads, ws)
+        want_rows, want, mags, cnt = ref.grad_rows(ids, f64(g), 1.0)
+        U = int(count)
+        assert np.array_equal(rows[:U].cpu().numpy(), want_rows)
+        assert (np.abs(f64(grads[:U]) - want) <= ref.grad_bound(mags, cnt)).all()
+
+
+def test_all_padded_none_and_values_at_padded_positions(ne):
+    """No row left: count 0, nothing written. NaN and infinities at padded positions are not
+    read into any sum."""
+    n, D = 300, 64
+    ws = ne.new_embedding_workspace(n, D)
+    rows, count = torch.full((n,), 8, dtype=torch.int32, device="cuda"), torch.full((1,), 8, dtype=torch.int32, device="cuda")
+    grads = torch.full((n, D), 8.0, device="cuda")
+    g = torch.full((n, D), float("nan"), device="cuda")
+    pads = torch.full((n,), 3, dtype=torch.int32, device="cuda")
+    ne.ngram_embedding_bwd_rows(pads, g, 10, rows, count, grads, ws, pad_id=3)
+    assert int(count) == 0 and bool((rows == 8).all()) and bool((grads == 8.0).all())
+    count.fill_(8)
+    ne.ngram_embedding_bwd_rows(pads[:0], g[:0], 10, rows[:0], count, grads[:0], ws)
+    assert int(count) == 0
+    rng = np.random.default_rng(0)
+    ids = rng.integers(0, 10, n).astype(np.int32)
+    gh = rng.standard_normal((n, D)).astype(np.float32)
+    gh[ids == 3] = np.inf
+    ok = gh.copy()
+    ok[ids == 3] = 0
+    out = []
+    for x in (gh, ok):
+        dense = torch.zeros((10, D), device="cuda")
+        ne.ngram_embedding_bwd(torch.from_numpy(ids).cuda(), torch.from_numpy(x).cuda(), dense, ws, pad_id=3)
+        out.append(dense)
+    assert torch.equal(out[0], out[1]) and bool((out[0][3] == 0).all())
+
+
+def test_gradient_bits_repeat_and_bad_ids_count_as_row_0(ne):
+    rng = np.random.default_rng(8)
+    n, V, D = 4000, 500, 264
+    ids = ids_of(rng, n, V, "zipf")
+    g = torch.from_numpy(rng.standard_normal((n, D))).to(BF16).cuda()
+    ws = ne.new_embedding_workspace(n, D)
+    first = check_rows(ne, ids, g, V, 1.0, -1, ws)
+    for _ in range(3):
+        again = check_rows(ne, ids, g, V, 1.0, -1, ws)
+        assert again[2] == first[2] and torch.equal(again[1], first[1])
+    bad, good = ids.copy(), ids.copy()
+    bad[::97], good[::97] = np.where(np.arange(len(bad[::97])) % 2, V, -4), 0
+    a, b = torch.zeros((V, D), device="cuda"), torch.zeros((V, D), device="cuda")
+    ne.ngram_embedding_bwd(torch.from_numpy(bad).cuda(), g, a, ws)
+    assert ne.ngram_embed_get_status(ws) == 0x1
+    ne.ngram_embed_clear_status(ws)
+    ne.ngram_embedding_bwd(torch.from_numpy(good).cuda(), g, b, ws)
+    assert torch.equal(a, b) and ne.ngram_embed_get_status(ws) == 0
+
+
+def test_gradient_of_strided_rows(ne):
+    rng = np.random.default_rng(6)
+    ids = ids_of(rng, 90, 20, "uniform")
+    for dtype, lo, width in ((BF16, 8, 160), (F32, 4, 148)):
+        buf = torch.from_numpy(rng.standard_normal((90, width))).to(dtype).cuda()
+        check_rows(ne, ids, buf[:, lo:lo + 136], 20, 1.25, -1)
+
+
+def test_gradient_is_the_lookup_s_by_differences(ne):
+    """Linear: (L(table + h E) - L(table)) / h = <dTable, E> for L = <lookup, g>, in 64 bits on
+    what the library returns for tables whose values fp32 holds exactly."""
+    rng = np.random.default_rng(13)
+    V, D, n = 30, 40, 200
+    ids = ids_of(rng, n, V, "zipf")
+    ids_d = torch.from_numpy(ids).cuda()
+    ws = ne.new_embedding_workspace(n, D)
+    base = rng.integers(-64, 65, (V, D)).astype(np.float32)
+    direction = rng.integers(-8, 9, (V, D)).astype(np.float32)
+    g = rng.integers(-16, 17, (n, D)).astype(np.float32)
+
+    def L(table):
+        out = torch.empty((n, D), device="cuda")
+        ne.ngram_embedding_fwd(torch.from_numpy(table).cuda(), ids_d, out, ws, scale=0.5, pad_id=2)
+        return float((f64(out) * g).sum())
+
+    d = torch.zeros((V, D), device="cuda")
+    ne.ngram_embedding_bwd(ids_d, torch.from_numpy(g).cuda(), d, ws, scale=0.5, pad_id=2)
+    assert L(base + direction) - L(base) == float((f64(d) * direction).sum())  # small integers and halves: exact
+
+
+def test_train_a_4bit_table_through_its_master(ne):
+    """Quantise a master, look it up, take the gradient as rows, update the touched master
+    rows, requantise: each step against the definitions on the values of the step before."""
+    rng = np.random.default_rng(77)
+    V, D, n = 200, 96, 500
+    master = torch.from_numpy(rng.standard_normal((V, D)) * 0.05).float().cuda()
+    q = ne.Mx4.empty(V, D)
+    ws = ne.new_embedding_workspace(n, D)
+    rows, count = torch.zeros(n, dtype=torch.int32, device="cuda"), torch.zeros(1, dtype=torch.int32, device="cuda")
+    grads = torch.zeros((n, D), device="cuda")
+    for step in range(3):
+        before = master.clone()
+        ne.ngram_mx4_quantize(master, q)
+        codes, scales = ref.quantise(f64(master))
+        assert np.array_equal(q.codes.cpu().numpy(), ref.pack(codes)) and np.array_equal(q.scales.cpu().numpy(), scales)
+        ids = ids_of(rng, n, V, "zipf")
+        ids_d = torch.from_numpy(ids).cuda()
+        out = torch.empty((n, D), dtype=BF16, device="cuda")
+        ne.ngram_embedding_fwd(q, ids_d, out, ws, scale=2.0)
+        assert np.array_equal(f64(out), ref.values(codes, scales)[ids] * 2.0)  # 4 bits times 2: exact in bf16
+        g = out - 1.0
+        ne.ngram_embedding_bwd_rows(ids_d, g, V, rows, count, grads, ws, scale=2.0)
+        want_rows, want, mags, cnt = ref.grad_rows(ids, f64(g), 2.0)
+        U = int(count)
+        assert np.array_equal(rows[:U].cpu().numpy(), want_rows)
+        assert (np.abs(f64(grads[:U]) - want) <= ref.grad_bound(mags, cnt)).all()
+        master[rows[:U].long()] -= 0.01 * grads[:U]
+        untouched = np.setdiff1d(np.arange(V), want_rows)
+        assert torch.equal(master[untouched], before[untouched])
+
+
+def test_gradient_captured_and_replayed(ne):
+    rng = np.random.default_rng(21)
+    n, V, D = 700, 300, 72
+    ids, g = torch.zeros(n, dtype=torch.int32, device="cuda"), torch.zeros((n, D), device="cuda")
+    ws = ne.new_embedding_workspace(n, D)
+    rows, count, grads = torch.zeros(n, dtype=torch.int32, device="cuda"), torch.zeros(1, dtype=torch.int32, device="cuda"), torch.zeros((n, D), device="cuda")
+    call = lambda: ne.ngram_embedding_bwd_rows(ids, g, V, rows, count, grads, ws, scale=1.5, pad_id=0)
+    call()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        call()
+    for k in range(3):
+        h = ids_of(rng, n, V, ("zipf", "uniform", "same")[k])
+        ids.copy_(torch.from_numpy(h).cuda())
+        g.copy_(torch.from_numpy(rng.standard_normal((n, D))).float().cuda())
+        graph.replay()
+        want_rows, want, mags, cnt = ref.grad_rows(h, f64(g), 1.5, 0)
+        U = int(count)
+        assert np.array_equal(rows[:U].cpu().numpy(), want_rows)
+        assert (np.abs(f64(grads[:U]) - want) <= ref.grad_bound(mags, cnt)).all()

@@ -1,0 +1,292 @@
+"""4-bit tables on the GPU: quantisation bit-exact, the product and the layer within the bound
+of their fp32 sums and one output rounding, against plain 64-bit definitions on the host."""
+import numpy as np
+import pytest
+import torch
+
+from synth import gen
+from tests import mx4_ref as ref
+
+pytestmark = pytest.mark.gpu
+
+BF16, F32 = torch.bfloat16, torch.float32
+HALF = {BF16: ref.BF16_HALF, F32: ref.F32_HALF}
+
+
+@pytest.fixture(scope="module")
+def ne():
+    import hashed_gram_embedding_horner_b200 as m
+    return m
+
+
+def f64(t):
+    return t.double().cpu().numpy()
+
+
+def device_mx4(ne, codes, scales, layout):
+    s = ref.tile_bytes(scales, fill=255) if layout == ne.MX4_TILES else scales  # rows past the last: NaN bytes
+    return ne.Mx4(torch.from_numpy(ref.pack(codes)).cuda(), torch.from_numpy(s).cuda(), codes.shape[0], codes.shape[1],
+                  layout)
+
+
+def special_rows(cols):
+    """Blocks of every special kind, tiled over a row of `cols`."""
+    z = np.zeros(32)
+    one = np.zeros(32)
+    one[5] = -1.0
+    ties = np.resize(np.array([6.0, 0.25, 0.75, 1.25, 1.75, 2.5, 3.5, 5.0, -0.25, -0.75, -1.25, -1.75, -2.5, -3.5, -5.0]), 32)
+    sat = np.resize(np.array([7.9375, 6.5, -7.0, 0.1]), 32)
+    tiny = np.resize(np.array([2.0 ** -126, -2.0 ** -130, 2.0 ** -133, 0.0]), 32)
+    huge = np.resize(np.array([3.3e38, -1e38, 1e30]), 32)
+    inf = one.copy()
+    inf[0] = np.inf
+    nan = one.copy()
+    nan[31] = np.nan
+    neg0 = -z
+    rows = [np.resize(np.concatenate([b, one]), cols) for b in (z, one, ties, sat, tiny, huge, inf, nan, neg0)]
+    return np.stack(rows)
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("rows,cols", [(1, 32), (3, 64), (130, 96), (257, 160), (9, 512)])
+def test_quantize_is_the_definition(ne, dtype, rows, cols):
+    rng = np.random.default_rng(rows * cols)
+    x = torch.from_numpy(rng.standard_normal((rows, cols)) * np.exp(2 * rng.standard_normal((rows, 1)))).to(dtype)
+    if rows == 9:
+        x = torch.from_numpy(special_rows(cols)).to(dtype)
+    codes, scales = ref.quantise(f64(x))
+    for layout in (ne.MX4_ROWS, ne.MX4_TILES):
+        q = ne.Mx4.empty(rows, cols, layout)
+        q.scales.fill_(77)  # rows past the last keep what was there
+        ne.ngram_mx4_quantize(x.cuda(), q)
+        assert np.array_equal(q.codes.cpu().numpy(), ref.pack(codes))
+        want = scales if layout == ne.MX4_ROWS else ref.tile_bytes(scales, fill=77)
+        assert np.array_equal(q.scales.cpu().numpy(), want)
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+def test_quantize_reads_strided_and_unaligned_rows(ne, dtype):
+    rng = np.random.default_rng(5)
+    buf = torch.from_numpy(rng.standard_normal((40, 331))).to(dtype).cuda()
+    for view in (buf[:, 8:72], buf[3:, 5:133], buf[::2, 1:33], buf[7:8, 3:35]):
+        codes, scales = ref.quantise(f64(view))
+        q = ne.Mx4.empty(view.shape[0], view.shape[1], ne.MX4_ROWS)
+        ne.ngram_mx4_quantize(view, q)
+        assert np.array_equal(q.codes.cpu().numpy(), ref.pack(codes)) and np.array_equal(q.scales.cpu().numpy(), scales)
+
+
+def test_quantising_what_a_quantised_row_stands_for_changes_nothing(ne):
+    x = torch.randn((70, 256), device="cuda")
+    q, r = ne.Mx4.empty(70, 256), ne.Mx4.empty(70, 256)
+    back = torch.empty((70, 256), device="cuda")
+    ne.ngram_mx4_quantize(x, q)
+    ne.ngram_embedding_fwd(q, None, back, ne.new_embedding_workspace(0, 256))
+    ne.ngram_mx4_quantize(back, r)
+    assert torch.equal(q.codes, r.codes) and torch.equal(q.scales, r.scales)
+
+
+@pytest.mark.parametrize("out_dtype", [BF16, F32])
+@pytest.mark.parametrize("M,N,K", [
+    (1, 1, 32), (1, 16, 64), (5, 7, 96), (2, 64, 128), (128, 128, 256), (129, 257, 288), (127, 65, 320), (64, 192, 512),
+    (33, 4096, 1024), (300, 1000, 2080), (640, 512, 4096), (1, 2048, 4096), (2000, 1536, 544),
+])
+def test_product_within_the_bound_of_its_sums(ne, M, N, K, out_dtype):
+    rng = np.random.default_rng(M * 7 + N * 3 + K)
+    a, b = ref.random_mx4(rng, M, K), ref.random_mx4(rng, N, K)
+    av, bv = ref.values(*a), ref.values(*b)
+    out = torch.full((M, N), 7.0, dtype=out_dtype, device="cuda")
+    ws = ne.new_mx4_workspace(M, N, K)
+    ne.ngram_mx4_product(device_mx4(ne, *a, ne.MX4_TILES), device_mx4(ne, *b, ne.MX4_TILES), out, ws, alpha=0.5)
+    assert ne.ngram_embed_get_status(ws) == 0
+    want = av @ bv.T * 0.5
+    assert (np.abs(f64(out) - want) <= ref.product_bound(av, bv * 0.5, HALF[out_dtype], want)).all()
+
+
+@pytest.mark.parametrize("out_dtype", [BF16, F32])
+def test_product_writes_only_its_own_columns(ne, out_dtype):
+    rng = np.random.default_rng(3)
+    a, b = ref.random_mx4(rng, 37, 96), ref.random_mx4(rng, 41, 96)
+    av, bv = ref.values(*a), ref.values(*b)
+    want = av @ bv.T
+    for lo, width in ((0, 64), (3, 57), (8, 72)):
+        buf = torch.full((39, width), 7.0, dtype=out_dtype, device="cuda")
+        out = buf[1:38, lo:lo + 41]
+        ne.ngram_mx4_product(device_mx4(ne, *a, ne.MX4_TILES), device_mx4(ne, *b, ne.MX4_TILES), out,
+                             ne.new_mx4_workspace(37, 41, 96))
+        assert (np.abs(f64(out) - want) <= ref.product_bound(av, bv, HALF[out_dtype], want)).all()
+        out.fill_(7.0)
+        assert bool((buf == 7.0).all())
+
+
+def test_product_carries_nan_blocks_and_wide_scales(ne):
+    """A NaN block makes its row (of A) or column (of B) NaN and nothing else; scales at the
+    ends of the range multiply as powers of two."""
+    rng = np.random.default_rng(9)
+    a, b = ref.random_mx4(rng, 130, 256), ref.random_mx4(rng, 70, 256)
+    a[1][129, 3] = 255
+    b[1][5, 0] = 255
+    out = torch.empty((130, 70), device="cuda")
+    ws = ne.new_mx4_workspace(130, 70, 256)
+    ne.ngram_mx4_product(device_mx4(ne, *a, ne.MX4_TILES), device_mx4(ne, *b, ne.MX4_TILES), out, ws)
+    av, bv = ref.values(*a), ref.values(*b)
+    got, want = f64(out), av @ bv.T
+    assert np.isnan(got[129]).all() and np.isnan(got[:, 5]).all()
+    ok = ~np.isnan(want)
+    assert ok.sum() == 129 * 69
+    assert (np.abs(got - want)[ok] <= ref.product_bound(np.nan_to_num(av), np.nan_to_num(bv), ref.F32_HALF,
+                                                        np.nan_to_num(want))[ok]).all()
+    a[1][:], b[1][:] = 0, 254  # 2^-127 and 2^127: the product's scales cancel
+    ne.ngram_mx4_product(device_mx4(ne, *a, ne.MX4_TILES), device_mx4(ne, *b, ne.MX4_TILES), out, ws)
+    av, bv = ref.values(*a), ref.values(*b)
+    want = av @ bv.T
+    assert (np.abs(f64(out) - want) <= ref.product_bound(av, bv, ref.F32_HALF, want)).all()
+
+
+def make_layer(ne, seed, V0, D, N, K, V, dtype):
+    rng = np.random.default_rng(seed)
+    S = (N - 1) * K
+    d = D // S
+    E = [ref.random_mx4(rng, v, d, spread=2) for v in V]
+    for e in E:
+        e[1][:] -= 5
+    W = ref.random_mx4(rng, D, D, spread=1)
+    W[1][:] -= 3
+    E0 = torch.from_numpy(rng.standard_normal((V0, D))).to(dtype).cuda()
+    plan = ne.ngram_embed_plan_create(V0, D, N, K, V, ne.NGRAM_BF16 if dtype == BF16 else ne.NGRAM_F32)
+    return dict(plan=plan, E0=E0, E=[device_mx4(ne, *e, ne.MX4_ROWS) for e in E], W=device_mx4(ne, *W, ne.MX4_TILES),
+                E_vals=[ref.values(*e) for e in E], W_vals=ref.values(*W))
+
+
+LAYERS = [  # V0, D, N, K, V, dtype
+    (50, 32, 2, 1, (61,), BF16),
+    (97, 96, 2, 3, (101, 103, 107), F32),
+    (1000, 512, 3, 2, (997, 1009, 1013, 1019), BF16),
+    (300, 1280, 5, 2, (211, 223, 227, 229, 233, 239, 241, 251), BF16),
+    (131, 288, 4, 1, (400, 401, 402), F32),
+    (131072, 1024, 3, 1, (3001, 3011), BF16),
+]
+
+
+@pytest.mark.parametrize("lengths", [[1], [5, 0, 1, 3], [127, 2], [100, 300, 0, 41], [1300]])
+@pytest.mark.parametrize("case", range(len(LAYERS)))
+def test_layer_from_4bit_tables(ne, case, lengths):
+    V0, D, N, K, V, dtype = LAYERS[case]
+    L = make_layer(ne, case, V0, D, N, K, V, dtype)
+    off = gen.offsets_from_lengths(lengths)
+    T = int(off[-1])
+    tokens = np.random.default_rng(T).integers(0, V0, T).astype(np.int32)
+    out = torch.full((T, D), 3.0, dtype=dtype, device="cuda")
+    ws = ne.new_embed_mx4_workspace(L["plan"], T)
+    ne.ngram_embed_plan_set_output_scale(L["plan"], 1.5)
+    ne.ngram_embed_fwd_mx4(L["plan"], torch.from_numpy(tokens).cuda(), torch.from_numpy(off).cuda(), L["E0"], L["E"],
+                           L["W"], out, ws)
+    assert ne.ngram_embed_get_status(ws) == 0
+    want, acc, _ = ref.layer(V0, N, K, V, tokens, off, f64(L["E0"]), L["E_vals"], L["W_vals"], out_scale=1.5)
+    assert (np.abs(f64(out) - want) <= acc + HALF[dtype] * (np.abs(want) + acc)).all()
+
+
+def test_layer_through_the_ring(ne):
+    """Decode: windows continue into each slot's committed history, also through other slots."""
+    V0, D, N, K, V, dtype = LAYERS[2]
+    L = make_layer(ne, 11, V0, D, N, K, V, dtype)
+    rng = np.random.default_rng(12)
+    B, C, P = 37, 8, 5
+    slots = rng.permutation(64)[:B].astype(np.int32)
+    hist = [rng.integers(0, V0, int(rng.integers(0, 9))).astype(np.int32) for _ in range(B)]
+    cache = ne.Cache.empty(64, C)
+    ws = ne.new_embed_mx4_workspace(L["plan"], B * P)
+    slots_d = torch.from_numpy(slots).cuda()
+    off_h = gen.offsets_from_lengths([len(h) for h in hist])
+    ne.ngram_cache_append(L["plan"], cache, torch.from_numpy(np.concatenate(hist).astype(np.int32)).cuda(),
+                          torch.from_numpy(off_h).cuda(), ws, slots=slots_d)
+    off = gen.offsets_from_lengths([P] * B)
+    tokens = rng.integers(0, V0, B * P).astype(np.int32)
+    out = torch.empty((B * P, D), dtype=dtype, device="cuda")
+    ne.ngram_embed_fwd_mx4(L["plan"], torch.from_numpy(tokens).cuda(), torch.from_numpy(off).cuda(), L["E0"], L["E"],
+                           L["W"], out, ws, cache=cache, cache_slots=slots_d)
+    assert ne.ngram_embed_get_status(ws) == 0
+    want, acc, _ = ref.layer(V0, N, K, V, tokens, off, f64(L["E0"]), L["E_vals"], L["W_vals"], histories=hist)
+    assert (np.abs(f64(out) - want) <= acc + HALF[dtype] * (np.abs(want) + acc)).all()
+
+
+def test_project_is_the_layer_given_its_indices_and_its_parts(ne):
+    """The same rows by the stand-alone operators: hash, lookup of each sub-table, requantise
+    (exact: the values are 4-bit already), product; then E_0 and the scale in 64 bits."""
+    V0, D, N, K, V, dtype = LAYERS[3]
+    S, d = 8, D // 8
+    L = make_layer(ne, 21, V0, D, N, K, V, dtype)
+    off = gen.offsets_from_lengths([150, 61])
+    T = 211
+    tokens = torch.from_numpy(np.random.default_rng(1).integers(0, V0, T).astype(np.int32)).cuda()
+    off_d = torch.from_numpy(off).cuda()
+    ws = ne.new_embed_mx4_workspace(L["plan"], T)
+    whole, parts = (torch.empty((T, D), dtype=dtype, device="cuda") for _ in range(2))
+    ne.ngram_embed_fwd_mx4(L["plan"], tokens, off_d, L["E0"], L["E"], L["W"], whole, ws)
+    idx = torch.empty((T, S), dtype=torch.int32, device="cuda")
+    ne.ngram_hash_indices(L["plan"], tokens, off_d, idx, ws)
+    ne.ngram_embed_project_mx4(L["plan"], tokens, idx, L["E0"], L["E"], L["W"], parts, ws)
+    assert torch.equal(whole, parts)
+    G = torch.empty((T, D), dtype=F32, device="cuda")
+    ews = ne.new_embedding_workspace(0, d)
+    for s in range(S):
+        ne.ngram_embedding_fwd(L["E"][s], idx[:, s].contiguous(), G[:, s * d:(s + 1) * d], ews)
+    q = ne.Mx4.empty(T, D, ne.MX4_TILES)
+    y = torch.empty((T, D), dtype=F32, device="cuda")
+    ne.ngram_mx4_quantize(G, q)
+    ne.ngram_mx4_product(q, L["W"], y, ne.new_mx4_workspace(T, D, D))
+    want = (L["E0"].double()[tokens.long()] + y.double()) / (S + 1)
+    mag = (G.double().abs() @ torch.from_numpy(np.abs(L["W_vals"])).cuda().T).cpu().numpy() / (S + 1)
+    bound = 2 * D * 2.0 ** -23 * mag + ref.BF16_HALF * np.abs(f64(want)) * 1.001 + 1e-30
+    assert (np.abs(f64(whole) - f64(want)) <= bound + 4 * ref.F32_HALF * np.abs(f64(want))).all()
+
+
+def test_bad_ids_set_the_status_and_read_row_0(ne):
+    V0, D, N, K, V, dtype = LAYERS[2]
+    L = make_layer(ne, 31, V0, D, N, K, V, dtype)
+    tokens = np.array([3, 4, 5], np.int32)
+    idx = np.array([[1, 2, 3, 4], [5, 6, 7, 8], [9, 10, 11, 12]], np.int32)
+    ws = ne.new_embed_mx4_workspace(L["plan"], 3)
+    run = lambda t, i: (lambda o: (ne.ngram_embed_project_mx4(L["plan"], torch.from_numpy(t).cuda(),
+                                                              torch.from_numpy(i).cuda(), L["E0"], L["E"], L["W"], o, ws),
+                                   o)[1])(torch.empty((3, D), dtype=dtype, device="cuda"))
+    for bad_t, bad_i in ((V0, 6), (-1, 6), (4, V[1]), (4, -7)):
+        t, i, t0, i0 = tokens.copy(), idx.copy(), tokens.copy(), idx.copy()
+        t[1], i[1, 1] = bad_t, bad_i
+        t0[1], i0[1, 1] = (bad_t if 0 <= bad_t < V0 else 0), (bad_i if 0 <= bad_i < V[1] else 0)
+        got = run(t, i)
+        assert ne.ngram_embed_get_status(ws) == 0x1
+        ne.ngram_embed_clear_status(ws)
+        assert torch.equal(got, run(t0, i0)) and ne.ngram_embed_get_status(ws) == 0
+
+
+def test_captured_replayed_and_on_another_stream(ne):
+    """Quantise and product captured once and replayed on new inputs, beside an eager call with
+    its own workspace on another stream."""
+    rng = np.random.default_rng(4)
+    w = ref.random_mx4(rng, 384, 512)
+    W = device_mx4(ne, *w, ne.MX4_TILES)
+    x = torch.randn((200, 512), device="cuda")
+    q, out, ws = ne.Mx4.empty(200, 512, ne.MX4_TILES), torch.empty((200, 384), device="cuda"), ne.new_mx4_workspace(200, 384, 512)
+
+    def step():
+        ne.ngram_mx4_quantize(x, q)
+        ne.ngram_mx4_product(q, W, out, ws)
+
+    step()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        step()
+    side = torch.cuda.Stream()
+    q2, out2, ws2 = ne.Mx4.empty(200, 512, ne.MX4_TILES), torch.empty((200, 384), device="cuda"), ne.new_mx4_workspace(200, 384, 512)
+    for k in range(3):
+        x.copy_(torch.randn((200, 512), device="cuda") * (k + 1))
+        torch.cuda.synchronize()
+        graph.replay()
+        ne.ngram_mx4_quantize(x, q2, stream=side)
+        ne.ngram_mx4_product(q2, W, out2, ws2, stream=side)
+        torch.cuda.synchronize()
+        assert torch.equal(out, out2)
+        av, bv = ref.values(*ref.quantise(f64(x))), ref.values(*w)
+        want = av @ bv.T
+        assert (np.abs(f64(out) - want) <= ref.product_bound(av, bv, ref.F32_HALF, want)).all()
