@@ -506,45 +506,61 @@ def new_workspace(plan: Plan, max_tokens: int, device="cuda"):
 
 
 # ---- 4-bit tables, and one table's lookup and gradient ----
+#
+# These calls are also made for a handful of tokens, where the host's share counts: tensors are
+# checked by cheap attributes, the ABI takes plain integers, and the stream is read directly.
 
-def _device_stream(stream, t):
-    """The given stream, or the current one of the tensor's own device."""
+_dtype_code = {}  # torch dtype -> NGRAM_*, filled by the first call
+_raw_stream = None
+
+
+def _load_torch():
+    global _raw_stream
     import torch
-    s = stream if stream is not None else torch.cuda.current_stream(t.device)
-    return ctypes.c_void_p(s.cuda_stream)
+    _dtype_code.update({torch.bfloat16: NGRAM_BF16, torch.float32: NGRAM_F32, torch.int32: "int32",
+                        torch.uint8: "uint8"})
+    _raw_stream = torch._C._cuda_getCurrentRawStream
 
 
-def _bytes_of(t):
-    return t.numel() * t.element_size()
+def _stream_of(stream, device: int) -> int:
+    """The given stream, or the current one of the tensors' own device."""
+    return stream.cuda_stream if stream is not None else _raw_stream(device)
 
 
-def _rows2d(t, name, device=None):
-    """A CUDA bf16 or f32 matrix with dense rows: its dtype code."""
-    import torch
-    code = {torch.bfloat16: NGRAM_BF16, torch.float32: NGRAM_F32}.get(t.dtype)
-    if code is None or not t.is_cuda or t.dim() != 2 or (t.shape[1] > 1 and t.numel() > 0 and t.stride(1) != 1):
-        raise NgramError(f"{name} must be a bf16 or f32 CUDA matrix with dense rows")
-    if device is not None and t.device != device:
-        raise NgramError(f"{name} is on {t.device}, not on {device}")
-    return code
+def _matrix(t, name, device=None):
+    """A CUDA bf16 or f32 matrix with dense rows: (dtype code, rows, columns, row stride)."""
+    if not _dtype_code:
+        _load_torch()
+    code = _dtype_code.get(t.dtype)
+    if not t.is_cuda or t.dim() != 2 or (code != NGRAM_BF16 and code != NGRAM_F32):
+        raise NgramError(f"{name} must be a bf16 or f32 CUDA matrix")
+    rows, cols = t.shape
+    s0, s1 = t.stride()
+    if s1 != 1 and cols > 1 and rows > 0:
+        raise NgramError(f"{name} must have dense rows")
+    if device is not None and t.get_device() != device:
+        raise NgramError(f"{name} is on cuda:{t.get_device()}, not on cuda:{device}")
+    return code, rows, cols, (s0 if rows > 1 else cols)  # a single row may carry any stride
 
 
-def _stride(t):
-    """Row stride in elements (a matrix of at most one row may carry any)."""
-    return max(t.stride(0), t.shape[1]) if t.shape[0] > 1 else t.shape[1]
+def _on(device, name, t):
+    if t.get_device() != device:
+        raise NgramError(f"{name} is not on cuda:{device}")
 
 
-def _on(device, **tensors):
-    for name, t in tensors.items():
-        if t is not None and t.device != device:
-            raise NgramError(f"{name} is on {t.device}, not on {device}")
-
-
-def _ids(t, name, n=None):
-    import torch
-    if t.dtype != torch.int32 or not t.is_cuda or not t.is_contiguous() or (n is not None and t.numel() != n):
+def _ids(t, name, device, n=None):
+    if not _dtype_code:
+        _load_torch()
+    if _dtype_code.get(t.dtype) != "int32" or not t.is_cuda or not t.is_contiguous() or (n is not None and t.numel() != n):
         raise NgramError(f"{name} must be a contiguous int32 CUDA tensor" + ("" if n is None else f" of {n} entries"))
-    return _ptr(t)
+    _on(device, name, t)
+    return t.data_ptr()
+
+
+def _space(workspace, device):
+    """A workspace's address and bytes."""
+    _on(device, "workspace", workspace)
+    return workspace.data_ptr(), workspace.numel() * workspace.element_size()
 
 
 class Mx4:
@@ -553,15 +569,18 @@ class Mx4:
     array of 512-byte tiles (MX4_TILES)."""
 
     def __init__(self, codes, scales, rows: int, cols: int, layout: int = MX4_ROWS):
-        import torch
-        need = _lib.ngram_mx4_scale_bytes(int(rows), int(cols), int(layout))
+        if not _dtype_code:
+            _load_torch()
+        rows, cols, layout = int(rows), int(cols), int(layout)
         if rows < 0 or cols < 1 or cols % 32 != 0 or layout not in (MX4_ROWS, MX4_TILES):
             raise NgramError("Mx4 needs rows >= 0, columns a multiple of 32 and a known layout")
-        for name, t, n in (("codes", codes, rows * cols // 2), ("scales", scales, need)):
-            if t.dtype != torch.uint8 or not t.is_cuda or not t.is_contiguous() or t.numel() != n:
+        for name, t, n in (("codes", codes, rows * cols // 2),
+                           ("scales", scales, _lib.ngram_mx4_scale_bytes(rows, cols, layout))):
+            if _dtype_code.get(t.dtype) != "uint8" or not t.is_cuda or not t.is_contiguous() or t.numel() != n:
                 raise NgramError(f"Mx4 {name} must be a contiguous uint8 CUDA tensor of {n} bytes")
-        _on(codes.device, scales=scales)
-        self.codes, self.scales, self.rows, self.cols, self.layout = codes, scales, int(rows), int(cols), int(layout)
+        self.device = codes.get_device()
+        _on(self.device, "scales", scales)
+        self.codes, self.scales, self.rows, self.cols, self.layout = codes, scales, rows, cols, layout
         self.struct = _Mx4(codes.data_ptr(), scales.data_ptr())
 
     @classmethod
@@ -575,17 +594,17 @@ class Mx4:
     def need(self, layout, what):
         if self.layout != layout:
             raise NgramError(f"{what} needs its scales {'in tiles' if layout == MX4_TILES else 'by rows'}")
-        return self
 
 
 def ngram_mx4_quantize(x, out: Mx4, stream=None):
     """Quantise the rows of x (bf16 or f32 [rows, cols], rows may be strided) into `out`."""
-    code = _rows2d(x, "x", out.codes.device)
-    if tuple(x.shape) != (out.rows, out.cols):
-        raise NgramError(f"x is {tuple(x.shape)}, out {(out.rows, out.cols)}")
-    rc = _lib.ngram_mx4_quantize(_ptr(x), code, out.rows, out.cols, _stride(x), _ptr(out.codes), _ptr(out.scales),
-                                 out.layout, _device_stream(stream, x))
-    _check(rc, "ngram_mx4_quantize")
+    code, rows, cols, stride = _matrix(x, "x", out.device)
+    if rows != out.rows or cols != out.cols:
+        raise NgramError(f"x is {(rows, cols)}, out {(out.rows, out.cols)}")
+    rc = _lib.ngram_mx4_quantize(x.data_ptr(), code, rows, cols, stride, out.struct.codes, out.struct.scales, out.layout,
+                                 _stream_of(stream, out.device))
+    if rc:
+        _check(rc, "ngram_mx4_quantize")
 
 
 def new_mx4_workspace(M: int, N: int, K: int, device="cuda"):
@@ -596,15 +615,19 @@ def new_mx4_workspace(M: int, N: int, K: int, device="cuda"):
 
 def ngram_mx4_product(a: Mx4, b: Mx4, out, workspace, alpha: float = 1.0, stream=None):
     """out = alpha * a b^T for a [M, K] and b [N, K] with scales in tiles (out bf16 or f32)."""
-    a.need(MX4_TILES, "a"), b.need(MX4_TILES, "b")
-    code = _rows2d(out, "out", a.codes.device)
-    _on(out.device, b=b.codes, workspace=workspace)
-    if a.cols != b.cols or tuple(out.shape) != (a.rows, b.rows):
-        raise NgramError(f"shapes do not fit: a {(a.rows, a.cols)}, b {(b.rows, b.cols)}, out {tuple(out.shape)}")
-    rc = _lib.ngram_mx4_product(ctypes.byref(a.struct), ctypes.byref(b.struct), a.rows, b.rows, a.cols, float(alpha),
-                                _ptr(out), code, _stride(out), _ptr(workspace), _bytes_of(workspace),
-                                _device_stream(stream, out))
-    _check(rc, "ngram_mx4_product")
+    a.need(MX4_TILES, "a")
+    b.need(MX4_TILES, "b")
+    dev = a.device
+    code, rows, cols, stride = _matrix(out, "out", dev)
+    if b.device != dev:
+        raise NgramError("a and b are on different devices")
+    if a.cols != b.cols or rows != a.rows or cols != b.rows:
+        raise NgramError(f"shapes do not fit: a {(a.rows, a.cols)}, b {(b.rows, b.cols)}, out {(rows, cols)}")
+    ws, ws_bytes = _space(workspace, dev)
+    rc = _lib.ngram_mx4_product(a.struct, b.struct, rows, cols, a.cols, alpha, out.data_ptr(), code, stride, ws, ws_bytes,
+                                _stream_of(stream, dev))
+    if rc:
+        _check(rc, "ngram_mx4_product")
 
 
 def new_embed_mx4_workspace(plan: Plan, max_tokens: int, device="cuda"):
@@ -616,45 +639,50 @@ def new_embed_mx4_workspace(plan: Plan, max_tokens: int, device="cuda"):
     return torch.zeros(n, dtype=torch.uint8, device=device)
 
 
-def _mx4_layer(plan: Plan, tokens, E0, E_nk, W: Mx4, out, workspace):
-    code = _rows2d(out, "out", tokens.device)
-    _rows2d(E0, "E0", tokens.device)
-    if code != plan.dtype or E0.dtype != out.dtype or not out.is_contiguous() or not E0.is_contiguous():
+def _mx4_layer(plan: Plan, n, E0, E_nk, W: Mx4, out, dev):
+    """Checks the layer's tensors; returns the array of the sub-tables' addresses."""
+    code, rows, cols, stride = _matrix(out, "out", dev)
+    code0, rows0, cols0, stride0 = _matrix(E0, "E0", dev)
+    if code != plan.dtype or code0 != plan.dtype or stride != cols or stride0 != cols0:
         raise NgramError("out and E0 must be contiguous and of the plan's dtype")
-    if tuple(out.shape) != (tokens.numel(), plan.D) or tuple(E0.shape) != (plan.V0, plan.D):
-        raise NgramError(f"out must be {(tokens.numel(), plan.D)} and E0 {(plan.V0, plan.D)}")
-    if len(E_nk) != plan.S or any((e.rows, e.cols) != (v, plan.d) for e, v in zip(E_nk, plan.V_nk)):
-        raise NgramError(f"E_nk must hold {plan.S} tables [V_nk, {plan.d}]")
-    if (W.rows, W.cols) != (plan.D, plan.D):
-        raise NgramError(f"W must be {(plan.D, plan.D)}")
+    if rows != n or cols != plan.D or rows0 != plan.V0 or cols0 != plan.D:
+        raise NgramError(f"out must be {(n, plan.D)} and E0 {(plan.V0, plan.D)}")
+    if len(E_nk) != plan.S or W.rows != plan.D or W.cols != plan.D or W.device != dev:
+        raise NgramError(f"the layer needs {plan.S} sub-tables and W {(plan.D, plan.D)} on out's device")
     W.need(MX4_TILES, "W")
-    _on(tokens.device, W=W.codes, workspace=workspace, **{f"E_nk[{s}]": e.need(MX4_ROWS, "E_nk").codes
-                                                         for s, e in enumerate(E_nk)})
-    return (_Mx4 * max(plan.S, 1))(*[e.struct for e in E_nk])
+    tabs = (_Mx4 * max(plan.S, 1))()
+    for s, (e, v) in enumerate(zip(E_nk, plan.V_nk)):
+        if e.rows != v or e.cols != plan.d or e.layout != MX4_ROWS or e.device != dev:
+            raise NgramError(f"E_nk[{s}] must be a table {(v, plan.d)} with scales by rows, on out's device")
+        tabs[s] = e.struct
+    return tabs
 
 
 def ngram_embed_fwd_mx4(plan: Plan, tokens, seq_offsets, E0, E_nk, W: Mx4, out, workspace, cache: Cache | None = None,
                         cache_slots=None, stream=None):
     """The layer from 4-bit sub-tables (Mx4 by rows) and a 4-bit W_stacked (Mx4 in tiles)."""
-    _ids(tokens, "tokens"), _ids(seq_offsets, "seq_offsets")
-    tabs = _mx4_layer(plan, tokens, E0, E_nk, W, out, workspace)
-    if cache_slots is not None:
-        _ids(cache_slots, "cache_slots", seq_offsets.numel() - 1)
-    rc = _lib.ngram_embed_fwd_mx4(plan.handle, _ptr(tokens), _ptr(seq_offsets), seq_offsets.numel() - 1, tokens.numel(),
-                                  _ptr(E0), tabs, ctypes.byref(W.struct), ctypes.byref(cache.struct) if cache else None,
-                                  _ptr(cache_slots), _ptr(out), _ptr(workspace), _bytes_of(workspace),
-                                  _device_stream(stream, out))
-    _check(rc, "ngram_embed_fwd_mx4")
+    dev = out.get_device()
+    n, seqs = tokens.numel(), seq_offsets.numel() - 1
+    tabs = _mx4_layer(plan, n, E0, E_nk, W, out, dev)
+    ws, ws_bytes = _space(workspace, dev)
+    rc = _lib.ngram_embed_fwd_mx4(plan.handle, _ids(tokens, "tokens", dev), _ids(seq_offsets, "seq_offsets", dev), seqs, n,
+                                  E0.data_ptr(), tabs, W.struct, ctypes.byref(cache.struct) if cache else None,
+                                  None if cache_slots is None else _ids(cache_slots, "cache_slots", dev, seqs),
+                                  out.data_ptr(), ws, ws_bytes, _stream_of(stream, dev))
+    if rc:
+        _check(rc, "ngram_embed_fwd_mx4")
 
 
 def ngram_embed_project_mx4(plan: Plan, tokens, idx, E0, E_nk, W: Mx4, out, workspace, stream=None):
     """That layer's projection, given the indices of ngram_hash_indices."""
-    _ids(tokens, "tokens"), _ids(idx, "idx", tokens.numel() * plan.S)
-    tabs = _mx4_layer(plan, tokens, E0, E_nk, W, out, workspace)
-    rc = _lib.ngram_embed_project_mx4(plan.handle, _ptr(tokens), _ptr(idx), tokens.numel(), _ptr(E0), tabs,
-                                      ctypes.byref(W.struct), _ptr(out), _ptr(workspace), _bytes_of(workspace),
-                                      _device_stream(stream, out))
-    _check(rc, "ngram_embed_project_mx4")
+    dev = out.get_device()
+    n = tokens.numel()
+    tabs = _mx4_layer(plan, n, E0, E_nk, W, out, dev)
+    ws, ws_bytes = _space(workspace, dev)
+    rc = _lib.ngram_embed_project_mx4(plan.handle, _ids(tokens, "tokens", dev), _ids(idx, "idx", dev, n * plan.S), n,
+                                      E0.data_ptr(), tabs, W.struct, out.data_ptr(), ws, ws_bytes, _stream_of(stream, dev))
+    if rc:
+        _check(rc, "ngram_embed_project_mx4")
 
 
 def new_embedding_workspace(max_ids: int, D: int, device="cuda"):
@@ -666,57 +694,60 @@ def new_embedding_workspace(max_ids: int, D: int, device="cuda"):
 def ngram_embedding_fwd(table, ids, out, workspace, scale: float = 1.0, pad_id: int = -1, stream=None):
     """out[i] = scale * table[ids[i]]; ids None: the table's first rows in order. The table is a
     contiguous bf16 or f32 matrix, or an Mx4 by rows; positions of pad_id get zeros."""
-    out_code = _rows2d(out, "out")
-    if isinstance(table, Mx4):
+    out_code, n, D, stride = _matrix(out, "out")
+    dev = out.get_device()
+    if type(table) is Mx4:
         table.need(MX4_ROWS, "table")
-        base, scales, code, V, D = table.codes, table.scales, NGRAM_MX4, table.rows, table.cols
+        if table.device != dev:
+            raise NgramError(f"table is not on cuda:{dev}")
+        base, scales, code, V, cols = table.struct.codes, table.struct.scales, NGRAM_MX4, table.rows, table.cols
     else:
-        code = _rows2d(table, "table")
-        if not table.is_contiguous():
+        code, V, cols, table_stride = _matrix(table, "table", dev)
+        if table_stride != cols:
             raise NgramError("table must be contiguous")
-        base, scales, V, D = table, None, table.shape[0], table.shape[1]
-    _on(out.device, table=base, workspace=workspace, ids=ids)
-    if out.shape[1] != D:
-        raise NgramError(f"out has {out.shape[1]} columns, the table {D}")
-    rc = _lib.ngram_embedding_fwd(_ptr(base), _ptr(scales), code, V, D,
-                                  None if ids is None else _ids(ids, "ids", out.shape[0]), out.shape[0], float(scale),
-                                  int(pad_id), _ptr(out), out_code, _stride(out), _ptr(workspace), _bytes_of(workspace),
-                                  _device_stream(stream, out))
-    _check(rc, "ngram_embedding_fwd")
+        base, scales = table.data_ptr(), None
+    if D != cols:
+        raise NgramError(f"out has {D} columns, the table {cols}")
+    ws, ws_bytes = _space(workspace, dev)
+    rc = _lib.ngram_embedding_fwd(base, scales, code, V, D, None if ids is None else _ids(ids, "ids", dev, n), n, scale,
+                                  pad_id, out.data_ptr(), out_code, stride, ws, ws_bytes, _stream_of(stream, dev))
+    if rc:
+        _check(rc, "ngram_embedding_fwd")
 
 
-def _f32_dense(t, name):
-    import torch
-    if t.dtype != torch.float32 or not t.is_cuda or not t.is_contiguous() or t.dim() != 2:
+def _f32_dense(t, name, device):
+    code, rows, cols, stride = _matrix(t, name, device)
+    if code != NGRAM_F32 or stride != cols:
         raise NgramError(f"{name} must be a contiguous f32 CUDA matrix")
-    return _ptr(t)
+    return rows, cols
 
 
 def ngram_embedding_bwd(ids, grad_out, d_table, workspace, scale: float = 1.0, pad_id: int = -1, stream=None):
     """d_table [V, D] (f32) += the lookup's gradient for grad_out [n, D] (bf16 or f32)."""
-    code = _rows2d(grad_out, "grad_out")
-    dt = _f32_dense(d_table, "d_table")
-    _on(grad_out.device, ids=ids, d_table=d_table, workspace=workspace)
-    if d_table.shape[1] != grad_out.shape[1]:
-        raise NgramError(f"d_table has {d_table.shape[1]} columns, grad_out {grad_out.shape[1]}")
-    n, D = grad_out.shape
-    rc = _lib.ngram_embedding_bwd(_ids(ids, "ids", n), n, _ptr(grad_out), code, _stride(grad_out), d_table.shape[0], D,
-                                  float(scale), int(pad_id), dt, _ptr(workspace), _bytes_of(workspace),
-                                  _device_stream(stream, grad_out))
-    _check(rc, "ngram_embedding_bwd")
+    code, n, D, stride = _matrix(grad_out, "grad_out")
+    dev = grad_out.get_device()
+    V, cols = _f32_dense(d_table, "d_table", dev)
+    if cols != D:
+        raise NgramError(f"d_table has {cols} columns, grad_out {D}")
+    ws, ws_bytes = _space(workspace, dev)
+    rc = _lib.ngram_embedding_bwd(_ids(ids, "ids", dev, n), n, grad_out.data_ptr(), code, stride, V, D, scale, pad_id,
+                                  d_table.data_ptr(), ws, ws_bytes, _stream_of(stream, dev))
+    if rc:
+        _check(rc, "ngram_embedding_bwd")
 
 
 def ngram_embedding_bwd_rows(ids, grad_out, V: int, rows, num_rows, grads, workspace, scale: float = 1.0,
                              pad_id: int = -1, stream=None):
     """The same gradient as rows: the distinct ids ascending in rows[:num_rows], their sums in
     grads[:num_rows] (f32); both hold room for n rows, num_rows is one int32 on the device."""
-    code = _rows2d(grad_out, "grad_out")
-    gr = _f32_dense(grads, "grads")
-    _on(grad_out.device, ids=ids, rows=rows, num_rows=num_rows, grads=grads, workspace=workspace)
-    n, D = grad_out.shape
-    if grads.shape[0] < n or grads.shape[1] != D or rows.numel() < n:
+    code, n, D, stride = _matrix(grad_out, "grad_out")
+    dev = grad_out.get_device()
+    room, cols = _f32_dense(grads, "grads", dev)
+    if room < n or cols != D or rows.numel() < n:
         raise NgramError(f"rows and grads need room for {n} rows of {D}")
-    rc = _lib.ngram_embedding_bwd_rows(_ids(ids, "ids", n), n, _ptr(grad_out), code, _stride(grad_out), int(V), D,
-                                       float(scale), int(pad_id), _ids(rows, "rows"), _ids(num_rows, "num_rows", 1), gr,
-                                       _ptr(workspace), _bytes_of(workspace), _device_stream(stream, grad_out))
-    _check(rc, "ngram_embedding_bwd_rows")
+    ws, ws_bytes = _space(workspace, dev)
+    rc = _lib.ngram_embedding_bwd_rows(_ids(ids, "ids", dev, n), n, grad_out.data_ptr(), code, stride, V, D, scale, pad_id,
+                                       _ids(rows, "rows", dev), _ids(num_rows, "num_rows", dev, 1), grads.data_ptr(), ws,
+                                       ws_bytes, _stream_of(stream, dev))
+    if rc:
+        _check(rc, "ngram_embedding_bwd_rows")

@@ -1,7 +1,8 @@
 // One table's lookup, out[i] = scale * table[ids[i]], and its gradient by sorted ids.
 //
-// Lookup: the table in bf16, f32 or mx4 (by rows, see mx4.cuh); eight elements a thread, the
-// next positions' loads in flight beside them.
+// Lookup: the table in bf16, f32 or mx4 (by rows, see mx4.cuh), a vector of eight elements at a
+// time (RowMap in mx4.cuh). Bound by HBM where its instructions leave it: an mx4 vector costs
+// about 60, most of them the decoding.
 //
 // Gradient: dTable[v] = scale * sum_{i : ids[i] = v} g_i. The positions are sorted by id with
 // a stable radix sort; runs of equal ids are summed in fp32 by whoever owns them, without
@@ -23,13 +24,12 @@ namespace ngram {
 enum TableType : int { kTableBf16 = 0, kTableF32 = 1, kTableMx4 = 2 };
 
 struct LookupParams {
+  RowMap map;             // positions of this launch x D / 8 vectors
   const void* table;      // bf16 / f32 rows, or mx4 codes
   const uint8_t* scales;  // mx4 scales by rows
   const int32_t* ids;     // [n], nullptr: row i
   uint32_t V;
   int64_t pad_id;         // positions with this id get a row of zeros (negative: none)
-  FastDiv per_row;        // D / 8
-  uint32_t vecs;          // n * D / 8 of this launch
   float scale;
   void* out;              // of position 0 of this launch, row stride out_stride elements
   int64_t out_stride;
@@ -37,20 +37,22 @@ struct LookupParams {
   int* status;
 };
 
-constexpr int kLookupUnroll = 4;
-
-// Eight E2M1 codes (low halves first) to floats.
+// Eight E2M1 codes (low halves first) to floats. The upper half of a code's fp32 is a function
+// of its four bits: byte permutations look up four magnitudes at once (high bytes
+// 00 3F 3F 3F 40 40 40 40, low bytes 00 00 80 C0 00 40 80 C0) and collect their signs. The
+// conversion instructions (E2M1 to f16, then f16 to f32) run at an eighth of that rate.
 __device__ __forceinline__ void e2m1x8(uint32_t codes, float (&x)[8]) {
+  const uint32_t up = codes << 4;
 #pragma unroll
-  for (int h = 0; h < 4; ++h) {
-    uint32_t f16;
-    asm("{\n\t.reg .b8 b;\n\tcvt.u8.u32 b, %1;\n\tcvt.rn.f16x2.e2m1x2 %0, b;\n\t}" : "=r"(f16) : "r"(codes >> (8 * h)));
-    float lo, hi;
-    asm("{\n\t.reg .b16 a, c;\n\tmov.b32 {a, c}, %2;\n\tcvt.f32.f16 %0, a;\n\tcvt.f32.f16 %1, c;\n\t}"
-        : "=f"(lo), "=f"(hi)
-        : "r"(f16));
-    x[2 * h] = lo;
-    x[2 * h + 1] = hi;
+  for (int h = 0; h < 2; ++h) {
+    const uint32_t sel = (codes >> (16 * h)) & 0x7777u;
+    const uint32_t sign = __byte_perm(up, codes, h ? 0x7362 : 0x5140) & 0x80808080u;  // of codes 0 .. 3, in their bytes
+    const uint32_t hi = __byte_perm(0x3F3F3F00u, 0x40404040u, sel) | sign, lo = __byte_perm(0xC0800000u, 0xC0804000u, sel);
+    const uint32_t m0 = __byte_perm(lo, hi, 0x5140), m1 = __byte_perm(lo, hi, 0x7362);  // codes 0, 1 and 2, 3
+    x[4 * h] = __uint_as_float(m0 << 16);
+    x[4 * h + 1] = __uint_as_float(m0 & 0xFFFF0000u);
+    x[4 * h + 2] = __uint_as_float(m1 << 16);
+    x[4 * h + 3] = __uint_as_float(m1 & 0xFFFF0000u);
   }
 }
 
@@ -73,76 +75,85 @@ __device__ __forceinline__ void store8(OutT* dst, const float (&x)[8]) {
   }
 }
 
-template <int TABLE, typename OutT>
+template <int TABLE, typename OutT, int U>
 __global__ void __launch_bounds__(256) lookup_kernel(const __grid_constant__ LookupParams p) {
-  const uint32_t base = blockIdx.x * (256u * kLookupUnroll) + threadIdx.x;
-  const uint32_t per_row = p.per_row.d;
-  int64_t row[kLookupUnroll];  // -1: zeros
-  uint32_t c[kLookupUnroll], pos[kLookupUnroll];
+  const RowPart<U> part(p.map);
+  if (!part.live) return;
+  constexpr int R = RowPart<U>::R;
+  uint4 raw[R][U][TABLE == kTableF32 ? 2 : 1];
+  uint32_t e[R][U];
+  bool zero[R];
 #pragma unroll
-  for (int u = 0; u < kLookupUnroll; ++u) {
-    const uint32_t v = base + u * 256u;
-    row[u] = -1;
-    if (v >= p.vecs) continue;
-    pos[u] = p.per_row.div(v);
-    c[u] = v - pos[u] * per_row;
-    if (!p.ids) {
-      row[u] = p.row0 + pos[u];
-      continue;
-    }
-    const int32_t id = __ldg(p.ids + pos[u]);
-    if (p.pad_id >= 0 && id == p.pad_id) continue;
-    row[u] = id;
-    if (static_cast<uint32_t>(id) >= p.V) {
-      set_status(p.status, NGRAM_STATUS_BAD_TOKEN);
-      row[u] = 0;
-    }
-  }
-  uint4 raw[kLookupUnroll][TABLE == kTableF32 ? 2 : 1];
-  uint32_t e[kLookupUnroll];
-#pragma unroll
-  for (int u = 0; u < kLookupUnroll; ++u) {
-    if (row[u] < 0) continue;
-    const size_t at = static_cast<size_t>(row[u]) * per_row + c[u];  // in units of eight elements
-    if constexpr (TABLE == kTableBf16) {
-      raw[u][0] = ld_stream_v4(static_cast<const uint16_t*>(p.table) + at * 8);
-    } else if constexpr (TABLE == kTableF32) {
-      raw[u][0] = ld_stream_v4(static_cast<const float*>(p.table) + at * 8);
-      raw[u][1] = ld_stream_v4(static_cast<const float*>(p.table) + at * 8 + 4);
-    } else {
-      raw[u][0].x = __ldg(static_cast<const uint32_t*>(p.table) + at);
-      e[u] = __ldg(p.scales + (at >> 2));
-    }
-  }
-#pragma unroll
-  for (int u = 0; u < kLookupUnroll; ++u) {
-    const uint32_t v = base + u * 256u;
-    if (v >= p.vecs) continue;
-    float x[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-    if (row[u] >= 0) {
-      if constexpr (TABLE == kTableBf16) {
-        const uint32_t w[4] = {raw[u][0].x, raw[u][0].y, raw[u][0].z, raw[u][0].w};
-#pragma unroll
-        for (int h = 0; h < 4; ++h) {
-          x[2 * h] = bf16_bits_to_float(w[h] & 0xFFFFu) * p.scale;
-          x[2 * h + 1] = bf16_bits_to_float(w[h] >> 16) * p.scale;
-        }
-      } else if constexpr (TABLE == kTableF32) {
-        const uint32_t w[8] = {raw[u][0].x, raw[u][0].y, raw[u][0].z, raw[u][0].w,
-                               raw[u][1].x, raw[u][1].y, raw[u][1].z, raw[u][1].w};
-#pragma unroll
-        for (int j = 0; j < 8; ++j) x[j] = __uint_as_float(w[j]) * p.scale;
-      } else {
-        // 2^k in two halves around the user's scale: each product by one is exact, so a value
-        // is rounded once, at the scale, and overflows only if the result does
-        float s1, s2;
-        e8m0_halves(e[u], s1, s2);
-        e2m1x8(raw[u][0].x, x);
-#pragma unroll
-        for (int j = 0; j < 8; ++j) x[j] = x[j] * s1 * p.scale * s2;
+  for (int r = 0; r < R; ++r) {
+    const uint32_t pos = part.row0 + r * part.row_step;
+    int64_t row = p.row0 + pos;
+    zero[r] = pos >= p.map.rows;
+    if (p.ids && !zero[r]) {
+      const int32_t id = __ldg(p.ids + pos);
+      zero[r] = p.pad_id >= 0 && id == p.pad_id;
+      row = id;
+      if (static_cast<uint32_t>(id) >= p.V && !zero[r]) {
+        set_status(p.status, NGRAM_STATUS_BAD_TOKEN);
+        row = 0;
       }
     }
-    store8<OutT>(static_cast<OutT*>(p.out) + static_cast<int64_t>(pos[u]) * p.out_stride + c[u] * 8, x);
+    const int64_t at = row * p.map.per_row + part.vec;  // in vectors of eight elements
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      if (zero[r] || part.vec + u * part.stride >= p.map.per_row) continue;
+      const int64_t v = at + u * part.stride;
+      if constexpr (TABLE == kTableBf16) {
+        raw[r][u][0] = ld_stream_v4(static_cast<const uint16_t*>(p.table) + v * 8);
+      } else if constexpr (TABLE == kTableF32) {
+        raw[r][u][0] = ld_stream_v4(static_cast<const float*>(p.table) + v * 8);
+        raw[r][u][1] = ld_stream_v4(static_cast<const float*>(p.table) + v * 8 + 4);
+      } else {
+        raw[r][u][0].x = __ldg(static_cast<const uint32_t*>(p.table) + v);
+        e[r][u] = __ldg(p.scales + (v >> 2));
+      }
+    }
+  }
+#pragma unroll
+  for (int r = 0; r < R; ++r) {
+    const uint32_t pos = part.row0 + r * part.row_step;
+    if (pos >= p.map.rows) continue;
+    OutT* out = static_cast<OutT*>(p.out) + static_cast<int64_t>(pos) * p.out_stride + part.vec * 8;
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      if (part.vec + u * part.stride >= p.map.per_row) continue;
+      float x[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+      if (!zero[r]) {
+        const uint4 a = raw[r][u][0];
+        if constexpr (TABLE == kTableBf16) {
+          const uint32_t w[4] = {a.x, a.y, a.z, a.w};
+#pragma unroll
+          for (int h = 0; h < 4; ++h) {
+            x[2 * h] = bf16_bits_to_float(w[h] & 0xFFFFu) * p.scale;
+            x[2 * h + 1] = __uint_as_float(w[h] & 0xFFFF0000u) * p.scale;
+          }
+        } else if constexpr (TABLE == kTableF32) {
+          const uint4 b = raw[r][u][1];
+          const uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+#pragma unroll
+          for (int j = 0; j < 8; ++j) x[j] = __uint_as_float(w[j]) * p.scale;
+        } else {
+          float s1, s2;
+          e8m0_halves(e[r][u], s1, s2);
+          e2m1x8(a.x, x);
+          const float f = s1 * p.scale * s2, m = fabsf(f);
+          if (m >= 0x1p-124f && m <= 0x1p124f) {  // scale * 2^k is exact: one rounding, at its product
+#pragma unroll
+            for (int j = 0; j < 8; ++j) x[j] *= f;
+          } else {
+            // 2^k in two halves around the scale: each product by one is exact, so a value is
+            // rounded once, at the scale, and overflows only if the result does
+#pragma unroll
+            for (int j = 0; j < 8; ++j) x[j] = x[j] * s1 * p.scale * s2;
+          }
+        }
+      }
+      store8<OutT>(out + u * part.stride * 8, x);
+    }
   }
 }
 
@@ -467,13 +478,18 @@ __global__ void __launch_bounds__(256) grad_reduce_kernel(const __grid_constant_
   else finish(cur);
 }
 
-// The runs that cross pieces: one warp a (piece whose last run begins in it and goes on, 256
-// columns) adds the partial sums in piece order.
+// The runs that cross pieces: one warp a (piece whose last run begins in it and goes on, 128
+// columns) adds the partial sums in piece order, kJoinLoads of them in flight: a frequent id's
+// run is hundreds of pieces long, and a warp alone waits for every load (4 in flight: 48 us for
+// 32768 Zipf ids at D = 4096).
+constexpr int kJoinLoads = 16;
+
 __global__ void __launch_bounds__(256) grad_join_kernel(const __grid_constant__ GradParams p) {
+  const int chunks = (p.D + 127) / 128;
   const uint64_t item = static_cast<uint64_t>(blockIdx.x) * 8 + (threadIdx.x >> 5);
   const int lane = threadIdx.x & 31;
-  const uint32_t piece = static_cast<uint32_t>(item / p.chunks);
-  const int c = static_cast<int>(item - static_cast<uint64_t>(piece) * p.chunks) * 256 + lane * 8;
+  const uint32_t piece = static_cast<uint32_t>(item / chunks);
+  const int c = static_cast<int>(item - static_cast<uint64_t>(piece) * chunks) * 128 + lane * 4;
   const uint64_t k0 = static_cast<uint64_t>(piece) * kGradPiece, k1 = k0 + kGradPiece;
   if (k1 >= p.n) return;
   const uint32_t key = p.key[k1 - 1];
@@ -487,22 +503,213 @@ __global__ void __launch_bounds__(256) grad_join_kernel(const __grid_constant__ 
     if (p.key[mid] == key) lo = mid; else hi = mid;
   }
   const uint32_t last = lo / kGradPiece;
-  float acc[8];
-  {
-    const float4* s = grad_partial(p, piece, 1, c);
-    const float4 a = __ldcg(s), b = __ldcg(s + 1);
-    acc[0] = a.x; acc[1] = a.y; acc[2] = a.z; acc[3] = a.w;
-    acc[4] = b.x; acc[5] = b.y; acc[6] = b.z; acc[7] = b.w;
-  }
-#pragma unroll 4
-  for (uint32_t q = piece + 1; q <= last; ++q) {
-    const float4* s = grad_partial(p, q, 0, c);
-    const float4 a = __ldcg(s), b = __ldcg(s + 1);
-    acc[0] += a.x; acc[1] += a.y; acc[2] += a.z; acc[3] += a.w;
-    acc[4] += b.x; acc[5] += b.y; acc[6] += b.z; acc[7] += b.w;
+  auto partial = [&](uint32_t q, int which) {
+    return reinterpret_cast<const float4*>(p.partial + (static_cast<size_t>(q) * 2 + which) * p.D + c);
+  };
+  float4 acc = __ldcg(partial(piece, 1));
+  for (uint32_t q0 = piece + 1; q0 <= last; q0 += kJoinLoads) {
+    float4 x[kJoinLoads];
+#pragma unroll
+    for (int k = 0; k < kJoinLoads; ++k)
+      if (q0 + k <= last) x[k] = __ldcg(partial(q0 + k, 0));
+#pragma unroll
+    for (int k = 0; k < kJoinLoads; ++k) {
+      if (q0 + k > last) break;
+      acc.x += x[k].x;
+      acc.y += x[k].y;
+      acc.z += x[k].z;
+      acc.w += x[k].w;
+    }
   }
   // the run's number: that of the next piece's beginning, which lies in it
-  grad_finish(p, p.piece_run[piece + 1], key, c, acc);
+  const int64_t row = p.dense ? static_cast<int64_t>(key) : p.piece_run[piece + 1];
+  float4* dst = reinterpret_cast<float4*>(p.out + row * p.D + c);
+  float4 y = make_float4(acc.x * p.scale, acc.y * p.scale, acc.z * p.scale, acc.w * p.scale);
+  if (p.dense) {
+    const float4 x = *dst;
+    y = make_float4(x.x + y.x, x.y + y.y, x.z + y.z, x.w + y.w);
+  }
+  *dst = y;
+}
+
+// ------------------------------------------------------------------ sort in one cluster
+//
+// Up to kClusterMax positions are sorted and their runs numbered in one launch, by a cluster of
+// CTAs that hold all of them in shared memory: each CTA ranks its kClusterItems positions by
+// digit, the CTAs exchange their digit counts, and every position is stored straight into its
+// place in the shared memory of the CTA that the place belongs to. Positions past n carry the
+// largest key, so they stay last. Measured for 32768 ids below 131072: 13 us, against 45 us of
+// launches and gaps for the tiled sort and the numbering kernels.
+
+constexpr int kClusterThreads = 1024;
+constexpr int kClusterItems = 4096;  // of one CTA: four a thread
+constexpr int kClusterCtas = 16;
+constexpr int kClusterMax = kClusterItems * kClusterCtas;
+constexpr int kClusterMaxBits = 9;
+
+struct ClusterSmem {
+  uint32_t key[kClusterItems];
+  int32_t pos[kClusterItems];
+  uint16_t warp_count[kClusterThreads / 32][1 << kClusterMaxBits];
+  uint32_t count[kClusterCtas][1 << kClusterMaxBits];  // of every CTA, pushed by it
+  uint32_t start[1 << kClusterMaxBits];
+  uint32_t heads[kClusterCtas];
+  uint32_t warp_sums[32];
+};
+
+struct ClusterSortParams {
+  SortParams s;    // ids, V, pad_id, n, bits; key_out and pos_out of the sorted positions
+  int passes;
+  GradParams r;    // rows_out, count_out, piece_run
+};
+
+__device__ __forceinline__ void st_cluster_u32(uint32_t addr, uint32_t v) {
+  asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(addr), "r"(v) : "memory");
+}
+__device__ __forceinline__ uint32_t ld_cluster_u32(uint32_t addr) {
+  uint32_t v;
+  asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(addr) : "memory");
+  return v;
+}
+
+// Every thread of the cluster. The block's own barrier comes first: it brings each warp together
+// again after the divergent code in front of it, which the aligned cluster barrier requires.
+__device__ __forceinline__ void cluster_barrier(uint32_t ctas) {
+  __syncthreads();
+  if (ctas > 1) cluster_sync();
+}
+
+// Exclusive scan of one value a thread over 1024 threads.
+__device__ __forceinline__ uint32_t cluster_block_scan(uint32_t x, uint32_t* warp_sums, uint32_t& total) {
+  const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
+  uint32_t s = x;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const uint32_t y = __shfl_up_sync(0xffffffffu, s, o);
+    if (lane >= o) s += y;
+  }
+  __syncthreads();  // warp_sums may still be read from the scan before
+  if (lane == 31) warp_sums[w] = s;
+  __syncthreads();
+  const uint32_t ws = warp_sums[lane];
+  uint32_t p = ws;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const uint32_t y = __shfl_up_sync(0xffffffffu, p, o);
+    if (lane >= o) p += y;
+  }
+  total = __shfl_sync(0xffffffffu, p, 31);
+  return __shfl_sync(0xffffffffu, p - ws, w) + s - x;
+}
+
+__global__ void __launch_bounds__(kClusterThreads, 1) sort_cluster_kernel(const __grid_constant__ ClusterSortParams a) {
+  extern __shared__ __align__(16) uint8_t cluster_raw[];
+  ClusterSmem& m = *reinterpret_cast<ClusterSmem*>(cluster_raw);
+  const SortParams& p = a.s;
+  const int tid = threadIdx.x, lane = tid & 31, w = tid >> 5;
+  const uint32_t rank = cluster_ctarank(), ctas = gridDim.x;
+  const int bins = 1 << p.bits;
+  const uint32_t base = rank * kClusterItems;
+  constexpr uint32_t kLast = 0xFFFFFFFFu;
+  uint32_t key[4];
+  int32_t pos[4];
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    const uint32_t i = base + w * 128 + j * 32 + lane;
+    key[j] = i < p.n ? sort_key(p, i, true) : kLast;
+    pos[j] = static_cast<int32_t>(i);
+  }
+  cluster_barrier(ctas);  // every CTA runs before its shared memory is written
+  for (int pass = 0; pass < a.passes; ++pass) {
+    const int shift = pass * p.bits;
+    uint32_t rk[4];
+    for (int b = lane; b < bins; b += 32) m.warp_count[w][b] = 0;
+    __syncwarp();
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const uint32_t dg = (key[j] >> shift) & (bins - 1);
+      const uint32_t peers = __match_any_sync(0xffffffffu, dg);
+      const uint32_t before = m.warp_count[w][dg];
+      __syncwarp();
+      rk[j] = before + __popc(peers & ((1u << lane) - 1u));
+      if (lane == __ffs(peers) - 1) m.warp_count[w][dg] = static_cast<uint16_t>(before + __popc(peers));
+      __syncwarp();
+    }
+    __syncthreads();
+    if (tid < bins) {  // the digit's ranks over the CTA's warps; its count to every CTA
+      uint32_t run = 0;
+#pragma unroll 8
+      for (int k = 0; k < kClusterThreads / 32; ++k) {
+        const uint32_t x = m.warp_count[k][tid];
+        m.warp_count[k][tid] = static_cast<uint16_t>(run);
+        run += x;
+      }
+      const uint32_t to = smem_u32(&m.count[rank][tid]);
+      for (uint32_t r = 0; r < ctas; ++r) st_cluster_u32(map_to_cta(to, r), run);
+    }
+    cluster_barrier(ctas);
+    uint32_t all = 0, lower = 0, ignored;
+    if (tid < bins)
+      for (uint32_t r = 0; r < ctas; ++r) {
+        const uint32_t x = m.count[r][tid];
+        if (r < rank) lower += x;
+        all += x;
+      }
+    const uint32_t smaller = cluster_block_scan(all, m.warp_sums, ignored);
+    if (tid < bins) m.start[tid] = smaller + lower;
+    __syncthreads();
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const uint32_t dg = (key[j] >> shift) & (bins - 1);
+      const uint32_t at = m.start[dg] + m.warp_count[w][dg] + rk[j];
+      const uint32_t cta = at / kClusterItems, in = at % kClusterItems;
+      st_cluster_u32(map_to_cta(smem_u32(&m.key[in]), cta), key[j]);
+      st_cluster_u32(map_to_cta(smem_u32(&m.pos[in]), cta), static_cast<uint32_t>(pos[j]));
+    }
+    cluster_barrier(ctas);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      key[j] = m.key[w * 128 + j * 32 + lane];
+      pos[j] = m.pos[w * 128 + j * 32 + lane];
+    }
+  }
+  // sorted: out, and the runs numbered, four neighbouring positions a thread
+  const uint32_t l0 = tid * 4;
+  uint32_t prev = l0 > 0 ? m.key[l0 - 1] : kLast;
+  const bool first = rank == 0 && tid == 0;
+  if (tid == 0 && rank > 0) prev = ld_cluster_u32(map_to_cta(smem_u32(&m.key[kClusterItems - 1]), rank - 1));
+  bool head[4];
+  uint32_t mine = 0, k4[4];
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    k4[j] = m.key[l0 + j];
+    head[j] = base + l0 + j < p.n && k4[j] < p.V && ((first && j == 0) || k4[j] != prev);
+    prev = k4[j];
+    mine += head[j] ? 1u : 0u;
+    if (base + l0 + j < p.n) {
+      p.key_out[base + l0 + j] = k4[j];
+      p.pos_out[base + l0 + j] = m.pos[l0 + j];
+    }
+  }
+  uint32_t total;
+  uint32_t run = cluster_block_scan(mine, m.warp_sums, total);
+  if (tid < static_cast<int>(ctas)) st_cluster_u32(map_to_cta(smem_u32(&m.heads[rank]), tid), total);
+  cluster_barrier(ctas);
+  uint32_t all = 0;
+  for (uint32_t r = 0; r < ctas; ++r) {
+    if (r < rank) run += m.heads[r];
+    all += m.heads[r];
+  }
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    const uint32_t i = base + l0 + j;
+    if (head[j]) {
+      if (a.r.rows_out) a.r.rows_out[run] = static_cast<int32_t>(k4[j]);
+      ++run;
+    }
+    if (i < p.n && i % kGradPiece == 0) a.r.piece_run[i / kGradPiece] = static_cast<int32_t>(run) - 1;
+  }
+  if (a.r.count_out && first) *a.r.count_out = static_cast<int32_t>(all);
 }
 
 }  // namespace ngram

@@ -39,6 +39,50 @@ struct FastDiv {
   }
 };
 
+// ------------------------------------------------------------------ work on rows of vectors
+//
+// How the row-wise kernels (quantisation, lookup) spread rows of `per_row` vectors of eight
+// elements over warps: a warp takes U vectors a lane along the columns of R = 4 / U rows (or
+// groups of rows where a row is narrower than a warp: 2^lg lanes a row), so the division that
+// finds its rows, the row addresses and the ids are paid once for four vectors a lane, and all
+// of a lane's loads are in flight together.
+struct RowMap {
+  uint32_t rows, per_row;  // vectors of eight elements a row
+  uint32_t lg;             // log2 of the lanes a row
+  FastDiv by_segs;         // column segments of a row: 2^lg * U vectors each
+  uint32_t items;          // warps
+  __host__ void set(uint32_t r, uint32_t vecs, int U) {
+    rows = r;
+    per_row = vecs;
+    lg = 0;
+    while (lg < 5 && (1u << lg) < vecs) ++lg;
+    const uint32_t segs = (vecs + (static_cast<uint32_t>(U) << lg) - 1) / (static_cast<uint32_t>(U) << lg);
+    by_segs.set(segs);
+    const uint32_t group = (32u >> lg) * static_cast<uint32_t>(4 / U);  // rows a warp
+    items = (r + group - 1) / group * segs;
+  }
+  // Columns a lane: as many as rows of this width fill.
+  __host__ static int unroll(uint32_t vecs) { return vecs >= 128 ? 4 : (vecs >= 64 ? 2 : 1); }
+};
+
+// A lane's part of warp `item`: rows row[0 .. 4/U) (a row past the last is not `on`), and its
+// first vector of a row; vector u is vec + u * stride.
+template <int U>
+struct RowPart {
+  static constexpr int R = 4 / U;
+  uint32_t row0, row_step, vec, stride;
+  bool live;  // the warp has work
+  __device__ __forceinline__ explicit RowPart(const RowMap& m) {
+    const uint32_t item = blockIdx.x * 8 + (threadIdx.x >> 5), lane = threadIdx.x & 31;
+    live = item < m.items;
+    const uint32_t rg = m.by_segs.div(item), seg = item - rg * m.by_segs.d;
+    row_step = 32u >> m.lg;
+    row0 = rg * row_step * R + (lane >> m.lg);
+    stride = 1u << m.lg;
+    vec = seg * (stride * U) + (lane & (stride - 1));
+  }
+};
+
 // ------------------------------------------------------------------ quantisation
 
 // Two floats to one byte of E2M1 codes: round to nearest, ties to even, saturating at 6;
@@ -50,10 +94,9 @@ __device__ __forceinline__ uint32_t e2m1x2(float lo, float hi) {
 }
 
 struct Mx4QuantParams {
+  RowMap map;
   const void* src;     // [rows x cols], row stride src_stride elements
   int64_t src_stride;
-  uint32_t vecs;       // rows * cols / 8 of this launch
-  FastDiv per_row;     // cols / 8
   int64_t row0;        // first row of this launch (tiles)
   int cols, kt;        // kt = ceil(cols / 128)
   uint8_t* codes;      // of row 0 of this launch
@@ -61,41 +104,47 @@ struct Mx4QuantParams {
   int tiles;           // 1: scales in tiles
 };
 
-constexpr int kMx4QuantUnroll = 4;
-
-// Eight elements of a row as floats; VEC: 16-byte loads.
+// Eight elements of a row, as they lie; VEC: 16-byte loads.
 template <typename T, bool VEC>
-__device__ __forceinline__ void mx4_load8(const T* src, float (&x)[8]) {
-  if constexpr (sizeof(T) == 2) {
-    uint32_t w[4];
-    if constexpr (VEC) {
-      const uint4 v = ld_stream_v4(src);
-      w[0] = v.x; w[1] = v.y; w[2] = v.z; w[3] = v.w;
-    } else {
+__device__ __forceinline__ void mx4_load8(const T* src, uint32_t (&w)[2 * sizeof(T)]) {
+  if constexpr (VEC) {
 #pragma unroll
-      for (int h = 0; h < 4; ++h) w[h] = src[2 * h] | (static_cast<uint32_t>(src[2 * h + 1]) << 16);
+    for (int h = 0; h < static_cast<int>(sizeof(T)) / 2; ++h) {
+      const uint4 v = ld_stream_v4(reinterpret_cast<const uint8_t*>(src) + 16 * h);
+      w[4 * h] = v.x;
+      w[4 * h + 1] = v.y;
+      w[4 * h + 2] = v.z;
+      w[4 * h + 3] = v.w;
     }
+  } else if constexpr (sizeof(T) == 2) {
 #pragma unroll
-    for (int h = 0; h < 4; ++h) {
-      x[2 * h] = bf16_bits_to_float(w[h] & 0xFFFFu);
-      x[2 * h + 1] = bf16_bits_to_float(w[h] >> 16);
-    }
+    for (int h = 0; h < 4; ++h) w[h] = src[2 * h] | (static_cast<uint32_t>(src[2 * h + 1]) << 16);
   } else {
-    if constexpr (VEC) {
-      const uint4 a = ld_stream_v4(src), b = ld_stream_v4(src + 4);
-      x[0] = __uint_as_float(a.x); x[1] = __uint_as_float(a.y); x[2] = __uint_as_float(a.z); x[3] = __uint_as_float(a.w);
-      x[4] = __uint_as_float(b.x); x[5] = __uint_as_float(b.y); x[6] = __uint_as_float(b.z); x[7] = __uint_as_float(b.w);
-    } else {
 #pragma unroll
-      for (int h = 0; h < 8; ++h) x[h] = src[h];
-    }
+    for (int h = 0; h < 8; ++h) w[h] = __float_as_uint(src[h]);
+  }
+}
+
+// The bits of the largest magnitude of eight elements, as fp32 (they order as the magnitudes
+// do, infinities and NaN above every number).
+template <typename T>
+__device__ __forceinline__ uint32_t mx4_amax8(const uint32_t (&w)[2 * sizeof(T)]) {
+  if constexpr (sizeof(T) == 2) {
+    uint32_t m = 0;
+#pragma unroll
+    for (int h = 0; h < 4; ++h) m = __vmaxu2(m, w[h] & 0x7FFF7FFFu);
+    return max(m << 16, m & 0xFFFF0000u);
+  } else {
+    uint32_t m = 0;
+#pragma unroll
+    for (int h = 0; h < 8; ++h) m = max(m, w[h] & 0x7FFFFFFFu);
+    return m;
   }
 }
 
 // A block's scale byte: two below the exponent of its largest magnitude (the exponent of
 // E2M1's largest power of two is 2), clamped to 2^-127; 0 for a block of zeros, 255 (NaN)
-// for a block that holds an infinity or a NaN. `amax` is the bits of the largest magnitude:
-// they order as the magnitudes do, infinities and NaN above every number.
+// for a block that holds an infinity or a NaN. `amax` as from mx4_amax8.
 __device__ __forceinline__ int mx4_scale_byte(uint32_t amax) {
   if (amax >= 0x7F800000u) return 255;
   const int e = static_cast<int>(amax >> 23) - 2;  // subnormal magnitudes: below 2^-126, clamped
@@ -106,57 +155,70 @@ __device__ __forceinline__ float mx4_inverse(int e) { return __uint_as_float(sta
 
 // Four lanes hold the 32 elements of a block, 8 each: the maximum by two shuffles, then one
 // conversion instruction for two elements; every lane's 16- or 32-byte load and 4-byte store
-// are part of a warp-wide contiguous access, and each thread has kMx4QuantUnroll of them in
-// flight. One pass: 2 or 4 bytes read and 17/32 written an element, bound by HBM.
-template <typename T, bool VEC>
+// are part of a warp-wide contiguous access. One pass: 2 or 4 bytes read and 17/32 written an
+// element, bound by HBM.
+template <typename T, bool VEC, int U>
 __global__ void __launch_bounds__(256) mx4_quantize_kernel(const __grid_constant__ Mx4QuantParams p) {
-  const T* src = static_cast<const T*>(p.src);
-  const uint32_t base = blockIdx.x * (256u * kMx4QuantUnroll) + threadIdx.x;
-  float x[kMx4QuantUnroll][8];
+  const RowPart<U> part(p.map);
+  if (!part.live) return;
+  constexpr int R = RowPart<U>::R;
+  uint32_t w[R][U][2 * sizeof(T)];
 #pragma unroll
-  for (int u = 0; u < kMx4QuantUnroll; ++u) {
-    const uint32_t v = base + u * 256u;
-    if (v < p.vecs) {
-      const uint32_t r = p.per_row.div(v), c = (v - r * p.per_row.d) * 8;
-      mx4_load8<T, VEC>(src + static_cast<int64_t>(r) * p.src_stride + c, x[u]);
-    }
+  for (int r = 0; r < R; ++r) {
+    const uint32_t row = part.row0 + r * part.row_step;
+    const T* src = static_cast<const T*>(p.src) + static_cast<int64_t>(row) * p.src_stride + part.vec * 8;
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+      if (row < p.map.rows && part.vec + u * part.stride < p.map.per_row) {
+        mx4_load8<T, VEC>(src + u * part.stride * 8, w[r][u]);
+      } else {
+#pragma unroll
+        for (int h = 0; h < static_cast<int>(2 * sizeof(T)); ++h) w[r][u][h] = 0;
+      }
   }
 #pragma unroll
-  for (int u = 0; u < kMx4QuantUnroll; ++u) {
-    const uint32_t v = base + u * 256u;
-    uint32_t amax = 0;
-    if (v < p.vecs) {
+  for (int r = 0; r < R; ++r) {
+    const uint32_t row = part.row0 + r * part.row_step;
+    const int64_t at = static_cast<int64_t>(row) * p.map.per_row + part.vec;  // in vectors
 #pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        const uint32_t m = __float_as_uint(x[u][j]) & 0x7FFFFFFFu;
-        amax = m > amax ? m : amax;
+    for (int u = 0; u < U; ++u) {
+      const uint32_t vec = part.vec + u * part.stride;
+      uint32_t amax = mx4_amax8<T>(w[r][u]);
+      amax = max(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
+      amax = max(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
+      if (row >= p.map.rows || vec >= p.map.per_row) continue;
+      const int e = mx4_scale_byte(amax);
+      uint32_t codes = 0;
+      if (e != 255) {
+        const float inv = mx4_inverse(e);
+        uint32_t c[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          float lo, hi;
+          if constexpr (sizeof(T) == 2) {
+            lo = bf16_bits_to_float(w[r][u][j] & 0xFFFFu);
+            hi = __uint_as_float(w[r][u][j] & 0xFFFF0000u);
+          } else {
+            lo = __uint_as_float(w[r][u][2 * j]);
+            hi = __uint_as_float(w[r][u][2 * j + 1]);
+          }
+          c[j] = e2m1x2(lo * inv, hi * inv);
+        }
+        codes = __byte_perm(__byte_perm(c[0], c[1], 0x0040), __byte_perm(c[2], c[3], 0x0040), 0x5410);
       }
-    }
-    uint32_t other = __shfl_xor_sync(0xffffffffu, amax, 1);
-    amax = other > amax ? other : amax;
-    other = __shfl_xor_sync(0xffffffffu, amax, 2);
-    amax = other > amax ? other : amax;
-    if (v >= p.vecs) continue;
-    const int e = mx4_scale_byte(amax);
-    uint32_t codes = 0;
-    if (e != 255) {
-      const float inv = mx4_inverse(e);
-#pragma unroll
-      for (int j = 0; j < 4; ++j) codes |= e2m1x2(x[u][2 * j] * inv, x[u][2 * j + 1] * inv) << (8 * j);
-    }
-    reinterpret_cast<uint32_t*>(p.codes)[v] = codes;
-    if ((v & 3u) == 0) {
-      if (!p.tiles) {
-        p.scales[v >> 2] = static_cast<uint8_t>(e);
-      } else {
-        const uint32_t r = p.per_row.div(v);
-        const int b = static_cast<int>(v - r * p.per_row.d) >> 2;
-        uint8_t* at = p.scales + mx4_tile_at(p.row0 + r, b, p.kt);
-        *at = static_cast<uint8_t>(e);
-        // the row's blocks end inside a tile: the rest of the tile's row is read as scales of
-        // zero codes, and must not be NaN
-        if (b == p.cols / kMxBlock - 1)
-          for (int k = 1; ((b + k) & 3) != 0; ++k) at[k] = 0;
+      reinterpret_cast<uint32_t*>(p.codes)[at + u * part.stride] = codes;
+      if ((vec & 3u) == 0) {
+        if (!p.tiles) {
+          p.scales[(at + u * part.stride) >> 2] = static_cast<uint8_t>(e);
+        } else {
+          const int b = static_cast<int>(vec >> 2);
+          uint8_t* to = p.scales + mx4_tile_at(p.row0 + row, b, p.kt);
+          *to = static_cast<uint8_t>(e);
+          // the row's blocks end inside a tile: the rest of the tile's row is read as scales of
+          // zero codes, and must not be NaN
+          if (b == p.cols / kMxBlock - 1)
+            for (int k = 1; ((b + k) & 3) != 0; ++k) to[k] = 0;
+        }
       }
     }
   }
@@ -242,15 +304,23 @@ __global__ void __launch_bounds__(256) mx4_gather_kernel(const __grid_constant__
 // tcgen05.cp (32 lanes x 16 bytes, repeated for the four lane quarters), issued by the MMA
 // thread in front of the stage's MMAs; the tensor pipe keeps their order.
 struct Mx4Maps {
-  CUtensorMap A;  // [M x K / 2] bytes, box 128 x 128 rows
-  CUtensorMap B;  // [N x K / 2] bytes, box 128 x BN rows
+  CUtensorMap A;   // [M x K / 2] bytes, box 128 x 128 rows
+  CUtensorMap B;   // [N x K / 2] bytes, box 128 x BN rows (pairs: BN / 2)
+  CUtensorMap At;  // boxes of the rows that the last box of A or B holds, to a multiple of 8:
+  CUtensorMap Bt;  // a box with many rows past the array's end takes far longer to fill
+  CUtensorMap SA;  // scale tiles as [row blocks x kt * 128] words, box 256 words (two tiles) x 1
+  CUtensorMap SB;  // the same of B, box 256 words x the tile's row blocks
 };
 
+// Rows of a box of `box` rows from `row` on that are loaded, of an array of `rows`: all of it,
+// the tail's, or none.
+__device__ __forceinline__ int mx4_box_rows(int rows, int row, int box) {
+  const int left = rows - row;
+  return left >= box ? box : (left <= 0 ? 0 : (left + 7) & ~7);
+}
+
 struct Mx4GemmParams {
-  const uint8_t* sa;  // scale tiles
-  const uint8_t* sb;
   int M, N, K;
-  int kt;             // ceil(K / 128): scale tiles of a row block
   int num_m_blocks, num_n_blocks, num_k_blocks;  // k-blocks of 256
   float scale;
   const int32_t* tokens;  // E_0 rows to add (nullptr: none)
@@ -258,24 +328,29 @@ struct Mx4GemmParams {
   uint32_t V0;
   void* out;
   int64_t ldo;            // elements
-  int vec;                // out rows admit 16-byte stores
+  int vec16, vec32;       // out and E_0 rows admit 16-byte, 32-byte accesses
   int* status;
 };
 
-constexpr int kMxThreads = 256;  // warp 0 loads, warp 1 MMA and TMEM, warps 4-7 epilogue
+constexpr int kMxEpiWarps = 8;
+constexpr int kMxStageWords = 32 * 9;  // of shared memory an epilogue warp: 32 bytes of 32 rows, padded
+constexpr int kMxThreads = 128 + 32 * kMxEpiWarps;  // warp 0 loads, warp 1 MMA and TMEM, warps 4-11 epilogue
 
-template <int BN, int STAGES>
+// PAIR: CTA pairs, 256 x BN tiles; each CTA holds its 128 rows of A with their scales, half of
+// B's rows, and the scales of all of B's rows.
+
+template <int BN, int STAGES, bool PAIR = false>
 struct Mx4Smem {
   static constexpr int kABytes = 128 * 128;
-  static constexpr int kBBytes = BN * 128;
+  static constexpr int kBBytes = (PAIR ? BN / 2 : BN) * 128;
   static constexpr int kSfbRows = BN > 128 ? BN / 128 : 1;  // row blocks of B's scales a tile touches
   static constexpr int kSfaOffset = kABytes + kBBytes;
   static constexpr int kSfbOffset = kSfaOffset + 2 * kMxTileBytes;
   static constexpr int kStageBytes = kSfbOffset + kSfbRows * 2 * kMxTileBytes;
   static constexpr int kBarOffset = STAGES * kStageBytes;
   static constexpr int kNumBars = 2 * STAGES + 5;
-  static constexpr int kEpiOffset = (kBarOffset + kNumBars * 8 + 16 + 127) / 128 * 128;
-  static constexpr int kBytes = kEpiOffset + 4 * 32 * 32 * 4;
+  static constexpr int kStgOffset = (kBarOffset + kNumBars * 8 + 16 + 15) / 16 * 16;
+  static constexpr int kBytes = kStgOffset + kMxEpiWarps * kMxStageWords * 4;
   static constexpr int kLaunchBytes = kBytes + 1024;
   static_assert(kStageBytes % 1024 == 0, "swizzled tiles start on 1024-byte boundaries");
   // TMEM: two accumulators and the stage's scales. At BN = 256 the accumulators share 32
@@ -317,6 +392,27 @@ __device__ __forceinline__ void tmem_cp_scales(uint32_t taddr, uint64_t desc) {
   asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(desc) : "memory");
 }
 
+// Pair forms: operands, scales and accumulators of both CTAs at the same addresses.
+__device__ __forceinline__ void umma_mx4_pair(uint32_t tmem_d, uint64_t adesc, uint64_t bdesc, uint32_t idesc,
+                                              uint32_t sfa, uint32_t sfb, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %6, 0;\n\t"
+      "tcgen05.mma.cta_group::2.kind::mxf4.block_scale.scale_vec::2X [%0], %1, %2, %3, [%4], [%5], p;\n\t}" ::"r"(tmem_d),
+      "l"(adesc), "l"(bdesc), "r"(idesc), "r"(sfa), "r"(sfb), "r"(accumulate)
+      : "memory");
+}
+__device__ __forceinline__ void tmem_cp_scales_pair(uint32_t taddr, uint64_t desc) {
+  asm volatile("tcgen05.cp.cta_group::2.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(desc) : "memory");
+}
+
+// One lane of a converged warp, the same one every time.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t on;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(on));
+  return on != 0;
+}
+
 // Descriptor of a scale tile: unswizzled, 8 rows of 16 bytes 128 bytes apart.
 __device__ __forceinline__ uint64_t scale_tile_desc(uint32_t saddr) {
   return static_cast<uint64_t>((saddr >> 4) & 0x3FFFu)
@@ -324,49 +420,203 @@ __device__ __forceinline__ uint64_t scale_tile_desc(uint32_t saddr) {
          | (static_cast<uint64_t>(1) << 46);        // descriptor version for sm_100
 }
 
-// Eight columns of an output row: x[j] (+ e0[j]) times scale, `n` of them inside the row.
+// 32-byte global accesses (sm_100: eight registers an instruction), 32-byte aligned.
+__device__ __forceinline__ void ld_global_v8(const void* p, uint32_t (&v)[8]) {
+  asm volatile("ld.global.nc.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+               : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7])
+               : "l"(p));
+}
+__device__ __forceinline__ void st_global_v8(void* p, const uint32_t (&v)[8]) {
+  asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(v[0]), "r"(v[1]), "r"(v[2]),
+               "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
+               : "memory");
+}
+
+// 32 columns of a row of E_0, as they lie, in 32-byte accesses: two (bf16) or four (f32).
 template <typename OutT>
-__device__ __forceinline__ void mx4_store8(OutT* dst, const float (&x)[8], const OutT* e0, float scale, int n, bool vec) {
-  if (vec && n >= 8) {
-    if constexpr (sizeof(OutT) == 2) {
-      uint32_t ew[4] = {0, 0, 0, 0};
-      if (e0) {
-        const uint4 e = __ldg(reinterpret_cast<const uint4*>(e0));
-        ew[0] = e.x; ew[1] = e.y; ew[2] = e.z; ew[3] = e.w;
-      }
-      uint32_t o[4];
+struct Mx4E0 {
+  static constexpr int kAcc = sizeof(OutT);
+  static constexpr int kCols = 32 / kAcc;
+  uint32_t v[kAcc][8];
+  // e0 at the first of the columns, nullptr: zeros
+  __device__ __forceinline__ void load(const OutT* e0, bool vec32) {
 #pragma unroll
-      for (int h = 0; h < 4; ++h)
-        o[h] = pack_bf16x2((x[2 * h] + bf16_bits_to_float(ew[h] & 0xFFFFu)) * scale,
-                           (x[2 * h + 1] + bf16_bits_to_float(ew[h] >> 16)) * scale);
-      *reinterpret_cast<uint4*>(dst) = make_uint4(o[0], o[1], o[2], o[3]);
-    } else {
+    for (int h = 0; h < kAcc; ++h) {
+      if (e0 && vec32) {
+        ld_global_v8(e0 + h * kCols, v[h]);
+      } else {
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        float4 e = make_float4(0.f, 0.f, 0.f, 0.f);
-        if (e0) e = __ldg(reinterpret_cast<const float4*>(e0) + h);
-        *(reinterpret_cast<float4*>(dst) + h) = make_float4((x[4 * h] + e.x) * scale, (x[4 * h + 1] + e.y) * scale,
-                                                             (x[4 * h + 2] + e.z) * scale, (x[4 * h + 3] + e.w) * scale);
+        for (int k = 0; k < 2; ++k) {
+          const uint4 x = e0 ? __ldg(reinterpret_cast<const uint4*>(e0 + h * kCols) + k) : make_uint4(0, 0, 0, 0);
+          v[h][4 * k] = x.x;
+          v[h][4 * k + 1] = x.y;
+          v[h][4 * k + 2] = x.z;
+          v[h][4 * k + 3] = x.w;
+        }
       }
     }
-  } else {
+  }
+};
+
+// The row of E_0 that output row `row` adds, or nullptr.
+template <typename OutT>
+__device__ __forceinline__ const OutT* mx4_e0_row(const Mx4GemmParams& p, int row) {
+  if (!p.tokens || row >= p.M) return nullptr;
+  uint32_t t = static_cast<uint32_t>(__ldg(p.tokens + row));
+  if (t >= p.V0) t = 0;
+  return static_cast<const OutT*>(p.E0) + static_cast<int64_t>(t) * p.N;
+}
+
+// 32 columns of 32 output rows (a row a lane) from col: (acc + E_0) * scale, rounded once. A lane
+// stores its own row, 32 bytes (a whole sector) an access, 16 where rows are less aligned.
+// Rows that admit neither, and the columns at a row's end, go through `stg` (kMxStageWords words
+// of the warp's own), a piece of 32 bytes a row at a time, so that neighbouring lanes store
+// neighbouring columns (a lane storing element by element took five times as long: 25 us for
+// 128 x 4090 at K = 4096, against 9 for 128 x 4096).
+template <typename OutT>
+__device__ __forceinline__ void mx4_store_rows(const Mx4GemmParams& p, int row0, int lane, int col, const uint32_t (&v)[32],
+                                               const Mx4E0<OutT>& e, uint32_t* stg) {
+  if (col >= p.N) return;
+  constexpr int kAcc = Mx4E0<OutT>::kAcc, kCols = Mx4E0<OutT>::kCols;
+  const int row = row0 + lane;
+  OutT* dst = static_cast<OutT*>(p.out) + static_cast<int64_t>(row) * p.ldo + col;
+#pragma unroll
+  for (int h = 0; h < kAcc; ++h) {
+    uint32_t o[8];
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
-      if (j >= n) break;
-      if constexpr (sizeof(OutT) == 2) {
-        const float e = e0 ? bf16_bits_to_float(e0[j]) : 0.f;
-        dst[j] = static_cast<uint16_t>(pack_bf16x2((x[j] + e) * scale, 0.f));
+      if constexpr (sizeof(OutT) == 2)
+        o[j] = pack_bf16x2((__uint_as_float(v[h * 16 + 2 * j]) + bf16_bits_to_float(e.v[h][j] & 0xFFFFu)) * p.scale,
+                           (__uint_as_float(v[h * 16 + 2 * j + 1]) + __uint_as_float(e.v[h][j] & 0xFFFF0000u)) * p.scale);
+      else
+        o[j] = __float_as_uint((__uint_as_float(v[h * 8 + j]) + __uint_as_float(e.v[h][j])) * p.scale);
+    }
+    const int left = p.N - col - h * kCols;  // columns inside the row
+    if (p.vec16 && left >= kCols) {
+      if (row >= p.M) continue;
+      if (p.vec32) {
+        st_global_v8(dst + h * kCols, o);
       } else {
-        dst[j] = (x[j] + (e0 ? e0[j] : 0.f)) * scale;
+        *reinterpret_cast<uint4*>(dst + h * kCols) = make_uint4(o[0], o[1], o[2], o[3]);
+        *reinterpret_cast<uint4*>(dst + h * kCols + kCols / 2) = make_uint4(o[4], o[5], o[6], o[7]);
       }
+    } else {
+#pragma unroll
+      for (int j = 0; j < 8; ++j) stg[lane * 9 + j] = o[j];
+      __syncwarp();
+      const OutT* in = reinterpret_cast<const OutT*>(stg);
+      constexpr int kPitch = 36 / static_cast<int>(sizeof(OutT));
+      const int c = lane % kCols;
+#pragma unroll
+      for (int i = 0; i < kCols; ++i) {
+        const int r = i * (32 / kCols) + lane / kCols;
+        if (row0 + r < p.M && c < left)
+          static_cast<OutT*>(p.out)[static_cast<int64_t>(row0 + r) * p.ldo + col + h * kCols + c] = in[r * kPitch + c];
+      }
+      __syncwarp();
     }
   }
 }
 
-template <int BN, int STAGES, typename OutT>
+// One tile's epilogue for one of the eight warps: TMEM lanes q * 32 .. + 31 (a row a lane), the
+// tile's column half g, 32 columns at a time: accumulators from TMEM, the row's E_0 added,
+// scaled, rounded and stored by the lane that holds them, 32 bytes (a whole sector) an access.
+// Nothing passes through shared memory, which the loads and the MMAs' operands keep busy. E_0
+// rows are random reads: the columns of all four chunks (bf16; two of them f32) are asked for
+// before the accumulator is ready, and the next tile's rows are brought toward L2.
+// `ready` waits for the accumulator (false: abort); `release` hands it back.
+template <typename L, int BN, typename OutT, typename Ready, typename Release>
+__device__ __forceinline__ bool mx4_epilogue(const Mx4GemmParams& p, uint32_t* stg, uint32_t tmem_base, int q, int g, int lane,
+                                             int row0, int col0, int next_row0, int next_col0, int acc, Ready ready,
+                                             Release release) {
+  constexpr int kChunks = BN / 64;
+  // The columns shared with the other accumulator go first: the last chunk of accumulator 0
+  // (of the half g = 1) or the first of accumulator 1 (g = 0). The other half has nothing to
+  // hand over and says so at once. Both only after this tile's accumulator is ready: an arrival
+  // before that could stand in for a slower warp's of the tile before.
+  const bool shares = L::kOverlap && g == (acc ^ 1);
+  const int rot = shares && g == 1 ? kChunks - 1 : 0;
+  const int row = row0 + lane;
+  auto chunk_col = [&](int cc) { return g * (BN / 2) + ((cc + rot) & (kChunks - 1)) * 32; };
+  constexpr int kInFlight = 8 / static_cast<int>(sizeof(OutT));
+  constexpr int kDepth = kChunks < kInFlight ? kChunks : kInFlight;  // chunks of E_0 in flight
+  Mx4E0<OutT> e[kDepth];
+  const OutT* e0 = mx4_e0_row<OutT>(p, row);
+  // N is a multiple of 32 where there is an E_0
+  auto load_e = [&](int slot, int col) { e[slot].load(e0 && col < p.N ? e0 + col : nullptr, p.vec32 != 0); };
+#pragma unroll
+  for (int cc = 0; cc < kDepth; ++cc) load_e(cc, col0 + chunk_col(cc));
+  if (const OutT* next = mx4_e0_row<OutT>(p, next_row0 + lane)) {  // the next tile's E_0, a row a lane
+    const int c0 = next_col0 + g * (BN / 2);
+#pragma unroll
+    for (int b = 0; b < BN / 2; b += 128 / static_cast<int>(sizeof(OutT)))
+      if (c0 + b < p.N) prefetch_l2(next + c0 + b);
+  }
+  if (!ready()) return false;
+  if (L::kOverlap && !shares) release();
+  const uint32_t taddr = tmem_base + (static_cast<uint32_t>(q * 32) << 16) + static_cast<uint32_t>(acc * L::kAccStride);
+#pragma unroll
+  for (int cc = 0; cc < kChunks; ++cc) {
+    uint32_t v[32];
+    tmem_ld_32x32b_x32(taddr + chunk_col(cc), v);
+    tmem_wait_ld();
+    if (L::kOverlap ? (cc == 0 && shares) : cc + 1 == kChunks) {
+      tc_fence_before();
+      release();
+    }
+    mx4_store_rows<OutT>(p, row0, lane, col0 + chunk_col(cc), v, e[cc % kDepth], stg);
+    if (cc + kDepth < kChunks) load_e(cc % kDepth, col0 + chunk_col(cc + kDepth));
+  }
+  return true;
+}
+
+// A stage's scale copies and MMAs (issued by one lane): K elements `left` from the stage's start
+// to the row's end (256 a stage), `first`: the sum starts here. col0: the tile's first column.
+template <typename L, int BN, bool PAIR>
+__device__ __forceinline__ void mx4_issue_stage(uint32_t at, uint32_t tmem_base, int col0, uint32_t d_tmem, int left,
+                                                bool first) {
+  constexpr uint32_t idesc0 = umma_idesc_mx4(PAIR ? 256 : 128, BN, 0), idesc1 = umma_idesc_mx4(PAIR ? 256 : 128, BN, 2);
+  const uint64_t adesc = sw128_kmajor_desc(at), bdesc = sw128_kmajor_desc(at + L::kABytes);
+  const uint64_t da = scale_tile_desc(at + L::kSfaOffset), db = scale_tile_desc(at + L::kSfbOffset);
+  const uint32_t sfa = tmem_base + L::kSfaCol;
+  // a tile narrower than a row block of scales starts inside its four columns
+  const uint32_t sfb = tmem_base + L::kSfbCol + (BN < 128 ? static_cast<uint32_t>((col0 & 127) >> 5) : 0u);
+  // scales of 128 elements of K, then their MMAs of 64
+  auto half = [&](int h, bool both) {
+    if (PAIR) tmem_cp_scales_pair(sfa + h * 4, da + h * (kMxTileBytes >> 4));
+    else tmem_cp_scales(sfa + h * 4, da + h * (kMxTileBytes >> 4));
+#pragma unroll
+    for (int r = 0; r < L::kSfbRows; ++r) {
+      const uint32_t to = tmem_base + L::kSfbCol + (h * L::kSfbRows + r) * 4;
+      if (PAIR) tmem_cp_scales_pair(to, db + (r * 2 + h) * (kMxTileBytes >> 4));
+      else tmem_cp_scales(to, db + (r * 2 + h) * (kMxTileBytes >> 4));
+    }
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+      if (k == 1 && !both) break;
+      const uint32_t fb = sfb + h * L::kSfbRows * 4, more = !first || h != 0 || k != 0 ? 1u : 0u;
+      const uint64_t ka = adesc + 2u * (2 * h + k), kbd = bdesc + 2u * (2 * h + k);
+      if (PAIR) umma_mx4_pair(d_tmem, ka, kbd, k ? idesc1 : idesc0, sfa + h * 4, fb, more);
+      else umma_mx4(d_tmem, ka, kbd, k ? idesc1 : idesc0, sfa + h * 4, fb, more);
+    }
+  };
+  if (left >= 256) {
+    half(0, true);
+    half(1, true);
+  } else {  // the last stage of a row may hold less
+    half(0, left > 64);
+    if (left > 128) half(1, left > 192);
+  }
+}
+
+// The kernel: one CTA a 128 x BN tile, or (PAIR) a cluster of two a 256 x BN tile. In a pair
+// every load signals CTA 0's stage barrier (.cta_group::2 loads, no multicast), one thread of
+// CTA 0 issues the copies of the scales and the MMAs for both, and its commits arrive in both.
+template <int BN, int STAGES, typename OutT, bool PAIR>
 __global__ void __launch_bounds__(kMxThreads, 1)
     mx4_gemm_kernel(const __grid_constant__ Mx4Maps maps, const __grid_constant__ Mx4GemmParams p) {
-  using L = Mx4Smem<BN, STAGES>;
+  using L = Mx4Smem<BN, STAGES, PAIR>;
+  constexpr int kRanks = PAIR ? 2 : 1;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   const uint32_t sbase = smem_u32(smem);
@@ -381,15 +631,19 @@ __global__ void __launch_bounds__(kMxThreads, 1)
   auto stage_at = [&](int s) { return sbase + s * L::kStageBytes; };
   const int warp = threadIdx.x >> 5;
   const int lane = threadIdx.x & 31;
+  const uint32_t rank = PAIR ? cluster_ctarank() : 0u;
+  auto wait = [&](uint32_t bar, uint32_t parity) {
+    return PAIR ? mbar_wait_cluster(bar, parity, abort_flag, p.status) : mbar_wait(bar, parity, abort_flag, p.status);
+  };
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < STAGES; ++s) {
-      mbar_init(full_bar(s), 1u);   // the producer's byte count
+      mbar_init(full_bar(s), 1u);   // CTA 0's producer's byte count
       mbar_init(empty_bar(s), 1u);  // one tcgen05.commit
     }
     for (int a = 0; a < 2; ++a) {
       mbar_init(tfull_bar(a), 1u);
-      mbar_init(tempty_bar(a), 128u);
+      mbar_init(tempty_bar(a), 32u * kMxEpiWarps + (PAIR ? kMxEpiWarps : 0));  // and CTA 1's warps, one arrival each
     }
     mbar_init(drain_bar, 1u);
     *abort_flag = 0;
@@ -399,19 +653,29 @@ __global__ void __launch_bounds__(kMxThreads, 1)
   if (warp == 0 && lane == 0) {
     tma_prefetch_desc(&maps.A);
     tma_prefetch_desc(&maps.B);
+    tma_prefetch_desc(&maps.At);
+    tma_prefetch_desc(&maps.Bt);
+    tma_prefetch_desc(&maps.SA);
+    tma_prefetch_desc(&maps.SB);
   }
   if (warp == 1) {
-    tmem_alloc(smem_u32(tmem_slot), L::kTmemCols);
-    tmem_relinquish();
+    if (PAIR) {
+      tmem_alloc_pair(smem_u32(tmem_slot), L::kTmemCols);
+      tmem_relinquish_pair();
+    } else {
+      tmem_alloc(smem_u32(tmem_slot), L::kTmemCols);
+      tmem_relinquish();
+    }
   }
   tc_fence_before();
   __syncthreads();
+  if (PAIR) cluster_sync();
   tc_fence_after();
   const uint32_t tmem_base = *tmem_slot;
 
   const int num_tiles = p.num_m_blocks * p.num_n_blocks;
   const int KB = p.num_k_blocks;
-  const int n_row_blocks = (p.N + 127) >> 7;
+  const int worker = blockIdx.x / kRanks, workers = gridDim.x / kRanks;
 
   if (warp == 0) {
     // ------------------------------------------------------------ TMA producer
@@ -420,23 +684,34 @@ __global__ void __launch_bounds__(kMxThreads, 1)
       int stage = 0;
       uint32_t phase = 0;
       bool ok = true;
-      for (int tile = blockIdx.x; tile < num_tiles && ok; tile += gridDim.x) {
-        const int m_blk = tile / p.num_n_blocks, n_blk = tile % p.num_n_blocks;
-        const int rb0 = n_blk * BN >> 7;  // first row block of B's scales
-        const int rbs = n_row_blocks - rb0 < L::kSfbRows ? n_row_blocks - rb0 : L::kSfbRows;
+      for (int tile = worker; tile < num_tiles && ok; tile += workers) {
+        const int m_blk = (tile / p.num_n_blocks) * kRanks + static_cast<int>(rank), n_blk = tile % p.num_n_blocks;
+        constexpr int kBRows = PAIR ? BN / 2 : BN;
+        const int brow = n_blk * BN + static_cast<int>(rank) * kBRows;
+        const int a_rows = mx4_box_rows(p.M, m_blk * 128, 128), b_rows = mx4_box_rows(p.N, brow, kBRows);
+        const void* map_a = a_rows == 128 ? &maps.A : &maps.At;
+        const void* map_b = b_rows == kBRows ? &maps.B : &maps.Bt;
+        uint32_t tx = kRanks * (L::kStageBytes - L::kABytes - L::kBBytes) + (a_rows + b_rows) * 128;
+        if (PAIR)  // rank 0 posts the bytes of both
+          tx += (mx4_box_rows(p.M, m_blk * 128 + 128, 128) + mx4_box_rows(p.N, brow + kBRows, kBRows)) * 128;
         for (int kb = 0; kb < KB; ++kb) {
-          if (!mbar_wait(empty_bar(stage), phase ^ 1u, abort_flag, p.status)) { ok = false; break; }
+          if (!wait(empty_bar(stage), phase ^ 1u)) { ok = false; break; }
           const uint32_t at = stage_at(stage);
-          // the last k-block may hold one scale tile of a row block instead of two
-          const uint32_t sbytes = (p.kt - 2 * kb >= 2 ? 2u : 1u) * kMxTileBytes;
-          mbar_arrive_expect_tx(full_bar(stage), L::kABytes + L::kBBytes + (1 + rbs) * sbytes);
-          tma_load_2d(at, &maps.A, kb * 128, m_blk * 128, full_bar(stage), pol);
-          tma_load_2d(at + L::kABytes, &maps.B, kb * 128, n_blk * BN, full_bar(stage), pol);
-          bulk_load_g2s(at + L::kSfaOffset, p.sa + (static_cast<size_t>(m_blk) * p.kt + 2 * kb) * kMxTileBytes, sbytes,
-                        full_bar(stage));
-          for (int r = 0; r < rbs; ++r)
-            bulk_load_g2s(at + L::kSfbOffset + r * 2 * kMxTileBytes,
-                          p.sb + (static_cast<size_t>(rb0 + r) * p.kt + 2 * kb) * kMxTileBytes, sbytes, full_bar(stage));
+          if (rank == 0) mbar_arrive_expect_tx(full_bar(stage), tx);
+          // bytes and scale tiles past the end of an array count and are filled with zeros
+          if (PAIR) {
+            const uint32_t bar = map_to_cta(full_bar(stage), 0);
+            if (a_rows) tma_load_2d_pair(at, map_a, kb * 128, m_blk * 128, bar, pol);
+            if (b_rows) tma_load_2d_pair(at + L::kABytes, map_b, kb * 128, brow, bar, pol);
+            tma_load_2d_pair(at + L::kSfaOffset, &maps.SA, kb * 256, m_blk, bar, pol);
+            tma_load_2d_pair(at + L::kSfbOffset, &maps.SB, kb * 256, n_blk * BN >> 7, bar, pol);
+          } else {
+            const uint32_t bar = full_bar(stage);
+            tma_load_2d(at, map_a, kb * 128, m_blk * 128, bar, pol);
+            tma_load_2d(at + L::kABytes, map_b, kb * 128, brow, bar, pol);
+            tma_load_2d(at + L::kSfaOffset, &maps.SA, kb * 256, m_blk, bar, pol);
+            tma_load_2d(at + L::kSfbOffset, &maps.SB, kb * 256, n_blk * BN >> 7, bar, pol);
+          }
           if (++stage == STAGES) { stage = 0; phase ^= 1u; }
         }
       }
@@ -446,132 +721,85 @@ __global__ void __launch_bounds__(kMxThreads, 1)
       }
     }
   } else if (warp == 1) {
-    // ------------------------------------------------------------ scales to TMEM, MMA
-    if (lane == 0) {
-      const uint32_t idesc[2] = {umma_idesc_mx4(128, BN, 0), umma_idesc_mx4(128, BN, 2)};
+    // ------------------------------------------------------------ scales to TMEM, MMA (CTA 0)
+    // The whole warp runs the loop, so that its addresses and descriptors are warp-uniform
+    // values, and one elected lane issues.
+    if (rank == 0 && elect_one()) {
       int stage = 0;
       uint32_t phase = 0;
       bool ok = true;
       int local = 0;
-      for (int tile = blockIdx.x; tile < num_tiles && ok; tile += gridDim.x, ++local) {
+      for (int tile = worker; tile < num_tiles && ok; tile += workers, ++local) {
         const int n_blk = tile % p.num_n_blocks;
         const int acc = local & 1;
         if (L::kOverlap) {  // the previous tile's shared columns have been drained
-          if (local > 0 && !mbar_wait(tempty_bar(0), (local - 1) & 1u, abort_flag, p.status)) { ok = false; break; }
+          if (local > 0 && !wait(tempty_bar(0), (local - 1) & 1u)) { ok = false; break; }
         } else {
-          if (!mbar_wait(tempty_bar(acc), ((local >> 1) & 1u) ^ 1u, abort_flag, p.status)) { ok = false; break; }
+          if (!wait(tempty_bar(acc), ((local >> 1) & 1u) ^ 1u)) { ok = false; break; }
         }
         tc_fence_after();
         const uint32_t d_tmem = tmem_base + static_cast<uint32_t>(acc * L::kAccStride);
-        const uint32_t sfa = tmem_base + L::kSfaCol;
-        const uint32_t sfb = tmem_base + L::kSfbCol;
-        // a tile narrower than a row block of scales starts inside its four columns
-        const uint32_t sfb_in = BN < 128 ? static_cast<uint32_t>((n_blk * BN & 127) >> 5) : 0u;
         for (int kb = 0; kb < KB; ++kb) {
-          if (!mbar_wait(full_bar(stage), phase, abort_flag, p.status)) { ok = false; break; }
+          if (!wait(full_bar(stage), phase)) { ok = false; break; }
           tc_fence_after();
-          const uint32_t at = stage_at(stage);
-          const int left = p.K - kb * 256;
-          const int steps = left >= 256 ? 4 : (left + 63) >> 6;
-#pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            if (2 * h >= steps) break;
-            tmem_cp_scales(sfa + h * 4, scale_tile_desc(at + L::kSfaOffset + h * kMxTileBytes));
-#pragma unroll
-            for (int r = 0; r < L::kSfbRows; ++r)
-              tmem_cp_scales(sfb + (h * L::kSfbRows + r) * 4,
-                             scale_tile_desc(at + L::kSfbOffset + (r * 2 + h) * kMxTileBytes));
+          {
+            mx4_issue_stage<L, BN, PAIR>(stage_at(stage), tmem_base, n_blk * BN, d_tmem, p.K - kb * 256, kb == 0);
+            if (PAIR) umma_commit_pair_both(empty_bar(stage));
+            else umma_commit(empty_bar(stage));
+            if (kb + 1 == KB) {
+              if (PAIR) umma_commit_pair_both(tfull_bar(acc));
+              else umma_commit(tfull_bar(acc));
+            }
           }
-          const uint64_t adesc = sw128_kmajor_desc(at);
-          const uint64_t bdesc = sw128_kmajor_desc(at + L::kABytes);
-#pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            if (k >= steps) break;
-            umma_mx4(d_tmem, adesc + 2u * k, bdesc + 2u * k, idesc[k & 1], sfa + (k >> 1) * 4,
-                     sfb + sfb_in + (k >> 1) * L::kSfbRows * 4, (kb | k) != 0 ? 1u : 0u);
-          }
-          umma_commit(empty_bar(stage));
           if (++stage == STAGES) { stage = 0; phase ^= 1u; }
         }
-        if (ok) umma_commit(tfull_bar(acc));
       }
-      umma_commit(drain_bar);
-      mbar_wait_drain(drain_bar, 0, 100ull * 1000 * 1000);
+      if (PAIR) umma_commit_pair_both(drain_bar);
+      else umma_commit(drain_bar);
     }
+    __syncwarp();
+    // the last commit: every MMA is done and, in CTA 1, every earlier commit's arrival has landed
+    mbar_wait_drain(drain_bar, 0, kWaitLimitNs);
+    __syncwarp();
   } else if (warp >= 4) {
-    // ------------------------------------------------------------ epilogue
-    // Per 32-column chunk: a row a lane from TMEM into the warp's staging area, then four
-    // lanes a row read it back, 8 columns each, so that every access to E_0 and out covers
-    // 8 rows x 64 (bf16) or 128 (f32) contiguous bytes. Staging: row r at r * 128 bytes,
-    // 16-byte unit w at (w ^ (r & 7)) * 16: no bank conflicts either way.
-    const int q = warp & 3;
-    const uint32_t stg = sbase + L::kEpiOffset + static_cast<uint32_t>(q) * 4096u;
-    const int rsub = lane >> 2, u2 = lane & 3;
-    const uint32_t row_w = stg + static_cast<uint32_t>(lane) * 128u;
-    const uint32_t rd_lo = stg + static_cast<uint32_t>(rsub) * 128u + (static_cast<uint32_t>((2 * u2) ^ rsub) << 4);
-    const uint32_t rd_hi = stg + static_cast<uint32_t>(rsub) * 128u + (static_cast<uint32_t>((2 * u2 + 1) ^ rsub) << 4);
+    // ------------------------------------------------------------ epilogue (own 128 rows)
+    const int q = warp & 3, g = (warp - 4) >> 2;
+    uint32_t* stg = reinterpret_cast<uint32_t*>(smem + L::kStgOffset) + (warp - 4) * kMxStageWords;
     int local = 0;
-    for (int tile = blockIdx.x; tile < num_tiles; tile += gridDim.x, ++local) {
-      const int m_blk = tile / p.num_n_blocks, n_blk = tile % p.num_n_blocks;
+    for (int tile = worker; tile < num_tiles; tile += workers, ++local) {
+      const int m_blk = (tile / p.num_n_blocks) * kRanks + static_cast<int>(rank), n_blk = tile % p.num_n_blocks;
       const int acc = local & 1;
-      const int row0 = m_blk * 128 + q * 32;
-      const OutT* e0[4];
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        e0[i] = nullptr;
-        const int gr = row0 + i * 8 + rsub;
-        if (p.tokens && gr < p.M) {
-          uint32_t t = static_cast<uint32_t>(p.tokens[gr]);
-          if (t >= p.V0) t = 0;
-          e0[i] = static_cast<const OutT*>(p.E0) + static_cast<int64_t>(t) * p.N;
+      auto ready = [&] {
+        bool got = false;
+        if (lane == 0) got = wait(tfull_bar(acc), (local >> 1) & 1u);
+        if (!__shfl_sync(0xffffffffu, got, 0)) return false;
+        tc_fence_after();
+        return true;
+      };
+      auto release = [&] {
+        const uint32_t bar = tempty_bar(L::kOverlap ? 0 : acc);
+        if (rank == 0) {
+          mbar_arrive_relaxed(bar);
+        } else {
+          __syncwarp();
+          if (lane == 0) mbar_arrive_remote_relaxed(map_to_cta(bar, 0));
         }
-      }
-      bool got = false;
-      if (lane == 0) got = mbar_wait(tfull_bar(acc), (local >> 1) & 1u, abort_flag, p.status);
-      if (!__shfl_sync(0xffffffffu, got, 0)) break;
-      tc_fence_after();
-      const uint32_t taddr = tmem_base + (static_cast<uint32_t>(q * 32) << 16) + static_cast<uint32_t>(acc * L::kAccStride);
-      constexpr int kChunks = BN / 32;
-#pragma unroll 1
-      for (int cc = 0; cc < kChunks; ++cc) {
-        // the columns shared with the other accumulator first: its last 32 (accumulator 0)
-        // or first 32 (accumulator 1)
-        const int c = L::kOverlap && acc == 0 ? (cc == 0 ? kChunks - 1 : cc - 1) : cc;
-        uint32_t v[32];
-        tmem_ld_32x32b_x32(taddr + c * 32, v);
-        tmem_wait_ld();
-        if (L::kOverlap ? cc == 0 : cc + 1 == kChunks) {
-          tc_fence_before();
-          mbar_arrive_relaxed(tempty_bar(L::kOverlap ? 0 : acc));
-        }
-#pragma unroll
-        for (int w = 0; w < 8; ++w)
-          st_shared_v4(row_w + (static_cast<uint32_t>(w ^ (lane & 7)) << 4),
-                       make_uint4(v[4 * w], v[4 * w + 1], v[4 * w + 2], v[4 * w + 3]));
-        __syncwarp();
-        const int col = n_blk * BN + c * 32 + u2 * 8;
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const uint4 lo = ld_shared_v4(rd_lo + i * 8 * 128);
-          const uint4 hi = ld_shared_v4(rd_hi + i * 8 * 128);
-          const int gr = row0 + i * 8 + rsub;
-          if (gr < p.M && col < p.N) {
-            const float x[8] = {__uint_as_float(lo.x), __uint_as_float(lo.y), __uint_as_float(lo.z), __uint_as_float(lo.w),
-                                __uint_as_float(hi.x), __uint_as_float(hi.y), __uint_as_float(hi.z), __uint_as_float(hi.w)};
-            mx4_store8<OutT>(static_cast<OutT*>(p.out) + static_cast<int64_t>(gr) * p.ldo + col, x,
-                             e0[i] ? e0[i] + col : nullptr, p.scale, p.N - col, p.vec != 0);
-          }
-        }
-        __syncwarp();  // the staging area is rewritten by the next chunk
-      }
+      };
+      const int next = tile + workers;
+      const int next_row0 = next < num_tiles ? ((next / p.num_n_blocks) * kRanks + static_cast<int>(rank)) * 128 + q * 32 : p.M;
+      if (!mx4_epilogue<L, BN, OutT>(p, stg, tmem_base, q, g, lane, m_blk * 128 + q * 32, n_blk * BN, next_row0,
+                                     (next % p.num_n_blocks) * BN, acc, ready, release))
+        break;
     }
   }
 
   tc_fence_before();
   __syncthreads();
+  if (PAIR) cluster_sync();  // no remote arrival or pair MMA is outstanding past this point
   if (warp == 1) {
     tc_fence_after();
-    tmem_dealloc(tmem_base, L::kTmemCols);
+    if (PAIR) tmem_dealloc_pair(tmem_base, L::kTmemCols);
+    else tmem_dealloc(tmem_base, L::kTmemCols);
   }
 }
 

@@ -4,6 +4,20 @@
 
 namespace {
 
+// A kernel's shared memory beyond 48 KB, asked for once a device (a bit of `done` each).
+template <typename K>
+int opt_in_smem(K kern, int bytes, std::atomic<uint64_t>& done, bool wide_clusters = false) {
+  int dev = -1;
+  if (cudaGetDevice(&dev) != cudaSuccess) return NGRAM_ERR_CUDA;
+  const uint64_t bit = uint64_t(1) << (dev & 63);
+  if (dev < 64 && (done.load(std::memory_order_acquire) & bit)) return NGRAM_OK;
+  if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes) != cudaSuccess ||
+      (wide_clusters && cudaFuncSetAttribute(kern, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) != cudaSuccess))
+    return NGRAM_ERR_CUDA;
+  if (dev < 64) done.fetch_or(bit, std::memory_order_release);
+  return NGRAM_OK;
+}
+
 // Makes the device that owns `p` current for a call, and the caller's again after it. Calls
 // without a plan take their device from a pointer; host memory is refused there.
 struct DeviceScope {
@@ -42,6 +56,8 @@ struct DeviceScope {
   DeviceScope& operator=(const DeviceScope&) = delete;
 };
 
+bool aligned32(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 31u) == 0; }
+
 int device_sms() {
   int dev = -1, sms = 0;
   if (cudaGetDevice(&dev) != cudaSuccess ||
@@ -69,38 +85,80 @@ int encode_codes(CUtensorMap* m, const void* base, int64_t cols, int64_t rows, i
   return r == CUDA_SUCCESS ? NGRAM_OK : NGRAM_ERR_CUDA;
 }
 
-template <int BN, int STAGES, typename OutT>
-int launch_mx4_tiles(Mx4GemmParams prm, const uint8_t* A, const uint8_t* B, int sms, cudaStream_t st) {
-  using L = Mx4Smem<BN, STAGES>;
-  static_assert(L::kLaunchBytes <= 232448, "4-bit product stages exceed 227 KB of shared memory");
-  auto kern = mx4_gemm_kernel<BN, STAGES, OutT>;
-  if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, L::kLaunchBytes) != cudaSuccess)
-    return NGRAM_ERR_CUDA;
-  Mx4Maps maps;
-  int rc = encode_codes(&maps.A, A, prm.K, prm.M, 128);
-  if (rc) return rc;
-  if ((rc = encode_codes(&maps.B, B, prm.K, prm.N, BN))) return rc;
-  prm.num_m_blocks = (prm.M + 127) / 128;
-  prm.num_n_blocks = (prm.N + BN - 1) / BN;
-  const int64_t tiles = static_cast<int64_t>(prm.num_m_blocks) * prm.num_n_blocks;
-  if (tiles > INT32_MAX / 2) return NGRAM_ERR_UNSUPPORTED;
-  const int grid = tiles < sms ? static_cast<int>(tiles) : sms;
-  return launch(kern, dim3(static_cast<unsigned>(grid)), dim3(kMxThreads), L::kLaunchBytes, st, false, 1, maps, prm);
+// 2-D map over scale tiles: [row blocks x kt * 128 words], boxes of two tiles x `blocks` row
+// blocks. Tiles and row blocks outside the array read zeros.
+int encode_scales(CUtensorMap* m, const void* base, int64_t rows, int64_t kt, int blocks) {
+  auto fn = encode_fn();
+  if (!fn) return NGRAM_ERR_CUDA;
+  const cuuint64_t dims[2] = {static_cast<cuuint64_t>(kt * 128), static_cast<cuuint64_t>((rows + 127) / 128)};
+  const cuuint64_t strides[1] = {static_cast<cuuint64_t>(kt * kMxTileBytes)};
+  const cuuint32_t box[2] = {256, static_cast<cuuint32_t>(blocks)};
+  const cuuint32_t estr[2] = {1, 1};
+  const CUresult r = fn(m, CU_TENSOR_MAP_DATA_TYPE_UINT32, 2, const_cast<void*>(base), dims, strides, box, estr,
+                        CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                        CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return r == CUDA_SUCCESS ? NGRAM_OK : NGRAM_ERR_CUDA;
 }
 
-template <typename OutT>
-int launch_mx4_gemm(Mx4GemmParams prm, const uint8_t* A, const uint8_t* B, int sms, cudaStream_t st) {
-  if (sms < 1) return NGRAM_ERR_CUDA;
-  prm.kt = (prm.K + 127) / 128;
+struct Mx4Operands {
+  const uint8_t *A, *SA, *B, *SB;  // codes and scale tiles
+};
+
+// The maps of a product whose tiles take 128 rows of A and b_rows of B a box (see Mx4Maps).
+int encode_mx4(Mx4Maps* m, const Mx4Operands& o, const Mx4GemmParams& p, int b_rows, int sfb_rows) {
+  const int64_t kt = (p.K + 127) / 128;
+  int rc;
+  if ((rc = encode_codes(&m->A, o.A, p.K, p.M, 128))) return rc;
+  if ((rc = encode_codes(&m->B, o.B, p.K, p.N, b_rows))) return rc;
+  m->At = m->A;
+  m->Bt = m->B;
+  if (p.M % 128 && (rc = encode_codes(&m->At, o.A, p.K, p.M, (p.M % 128 + 7) & ~7))) return rc;
+  if (p.N % b_rows && (rc = encode_codes(&m->Bt, o.B, p.K, p.N, (p.N % b_rows + 7) & ~7))) return rc;
+  if ((rc = encode_scales(&m->SA, o.SA, p.M, kt, 1))) return rc;
+  return encode_scales(&m->SB, o.SB, p.N, kt, sfb_rows);
+}
+
+template <int BN, int STAGES, typename OutT, bool PAIR>
+int launch_mx4_tiles(Mx4GemmParams prm, const Mx4Operands& o, int sms, cudaStream_t st) {
+  using L = Mx4Smem<BN, STAGES, PAIR>;
+  static_assert(L::kLaunchBytes <= 232448, "4-bit product stages exceed 227 KB of shared memory");
+  auto kern = mx4_gemm_kernel<BN, STAGES, OutT, PAIR>;
+  static std::atomic<uint64_t> done{0};
+  Mx4Maps maps;
+  int rc = opt_in_smem(kern, L::kLaunchBytes, done);
+  if (rc) return rc;
+  if ((rc = encode_mx4(&maps, o, prm, PAIR ? BN / 2 : BN, L::kSfbRows))) return rc;
+  constexpr int kRows = PAIR ? 256 : 128;
+  prm.num_m_blocks = (prm.M + kRows - 1) / kRows;
+  prm.num_n_blocks = (prm.N + BN - 1) / BN;
   prm.num_k_blocks = (prm.K + 255) / 256;
-  // the width whose waves of tiles bring in the fewest bytes an SM: (128 + BN) rows a tile
-  auto cost = [&](int bn) {
-    const int64_t tiles = static_cast<int64_t>((prm.M + 127) / 128) * ((prm.N + bn - 1) / bn);
-    return (tiles + sms - 1) / sms * (128 + bn);
+  const int64_t tiles = static_cast<int64_t>(prm.num_m_blocks) * prm.num_n_blocks;
+  if (tiles > INT32_MAX / 2) return NGRAM_ERR_UNSUPPORTED;
+  const int workers = PAIR ? sms / 2 : sms;
+  const int grid = (tiles < workers ? static_cast<int>(tiles) : workers) * (PAIR ? 2 : 1);
+  return launch(kern, dim3(static_cast<unsigned>(grid)), dim3(kMxThreads), L::kLaunchBytes, st, false, PAIR ? 2 : 1, maps,
+                prm);
+}
+
+// Which tiles: CTA pairs on 256 x 256, or one CTA on 128 x 128 or 128 x 64. The pairs' tiles
+// bring in the fewest bytes for their products, and a pass of a wave over a k-block takes about
+// 0.42 us, against 0.33 and 0.29 us for the narrower ones; those fill the SMs where the wide
+// ones are too few. Measured on B200, bf16 out (us, wide / 128 / 64): 32768 x 4096 x 4096 206 /
+// 310 / 548, 1280 x 4096 x 4096 17.3 / 20.2 / 28.2, 512 x 4096 x 4096 11.3 / 9.6 / 13.5,
+// 333 x 1111 x 2080 11.6 / 8.7 / 6.6, 128 x 512 x 512 6.8 / 4.7 / 4.0.
+template <typename OutT>
+int launch_mx4_gemm(const Mx4GemmParams& prm, const Mx4Operands& o, int sms, cudaStream_t st) {
+  if (sms < 2) return NGRAM_ERR_CUDA;
+  const double kb = (prm.K + 255) / 256;
+  auto cost = [&](int rows, int cols, int workers, double us_kb, double us_tile) {
+    const int64_t tiles = static_cast<int64_t>((prm.M + rows - 1) / rows) * ((prm.N + cols - 1) / cols);
+    return static_cast<double>((tiles + workers - 1) / workers) * (kb * us_kb + us_tile);
   };
-  if (cost(256) <= cost(128) && cost(256) <= cost(64)) return launch_mx4_tiles<256, 4, OutT>(prm, A, B, sms, st);
-  if (cost(128) <= cost(64)) return launch_mx4_tiles<128, 6, OutT>(prm, A, B, sms, st);
-  return launch_mx4_tiles<64, 7, OutT>(prm, A, B, sms, st);
+  const double wide = cost(256, 256, sms / 2, 0.42, 1.6), mid = cost(128, 128, sms, 0.33, 1.0),
+               narrow = cost(128, 64, sms, 0.29, 0.5);
+  if (wide <= mid && wide <= narrow) return launch_mx4_tiles<256, 6, OutT, true>(prm, o, sms, st);
+  if (mid <= narrow) return launch_mx4_tiles<128, 6, OutT, false>(prm, o, sms, st);
+  return launch_mx4_tiles<64, 8, OutT, false>(prm, o, sms, st);
 }
 
 // Workspace of the layer on 4-bit tables: [head | T x S indices | T x D / 2 codes | scale tiles]
@@ -164,8 +222,6 @@ int project_mx4(const ngram_embed_plan* p, const int32_t* tokens, const int32_t*
                   p->pdl, 1, g);
   if (rc) return rc;
   Mx4GemmParams prm{};
-  prm.sa = w.Gs;
-  prm.sb = static_cast<const uint8_t*>(W->scales);
   prm.M = static_cast<int>(T);
   prm.N = p->D;
   prm.K = p->D;
@@ -175,11 +231,11 @@ int project_mx4(const ngram_embed_plan* p, const int32_t* tokens, const int32_t*
   prm.V0 = static_cast<uint32_t>(p->V0);
   prm.out = out;
   prm.ldo = p->D;
-  prm.vec = 1;  // D * element size is a multiple of 16, as out's address
+  prm.vec16 = 1;  // rows of a multiple of 32 elements, out and E_0 16-byte aligned
+  prm.vec32 = aligned32(out) && aligned32(E0) ? 1 : 0;
   prm.status = status_ptr(ws);
-  const auto* Wc = static_cast<const uint8_t*>(W->codes);
-  return p->dtype == NGRAM_F32 ? launch_mx4_gemm<float>(prm, w.G, Wc, p->sms, st)
-                               : launch_mx4_gemm<uint16_t>(prm, w.G, Wc, p->sms, st);
+  const Mx4Operands o{w.G, w.Gs, static_cast<const uint8_t*>(W->codes), static_cast<const uint8_t*>(W->scales)};
+  return p->dtype == NGRAM_F32 ? launch_mx4_gemm<float>(prm, o, p->sms, st) : launch_mx4_gemm<uint16_t>(prm, o, p->sms, st);
 }
 
 // ---- lookup and gradient of one table ----
@@ -238,10 +294,12 @@ int embedding_bwd(const int32_t* ids, int64_t n, const void* g, int g_dtype, int
     if (!dense && cudaMemsetAsync(count_out, 0, 4, st) != cudaSuccess) return NGRAM_ERR_CUDA;
     return NGRAM_OK;
   }
-  // keys 0 .. V (V: a padded position), in equal digits of at most kSortMaxBits bits
+  // keys 0 .. V (V: a padded position) in equal digits
   int bits = 1;
   while ((V >> bits) != 0) ++bits;
-  const int passes = (bits + kSortMaxBits - 1) / kSortMaxBits;
+  const bool cluster = n <= kClusterMax;
+  const int max_bits = cluster ? kClusterMaxBits : kSortMaxBits;
+  const int passes = (bits + max_bits - 1) / max_bits;
   SortParams s{};
   s.ids = ids;
   s.V = static_cast<uint32_t>(V);
@@ -252,21 +310,7 @@ int embedding_bwd(const int32_t* ids, int64_t n, const void* g, int g_dtype, int
   s.counts = w.counts;
   s.totals = w.totals;
   s.status = status_ptr(workspace);
-  int rc, cur = 0;
-  for (int k = 0; k < passes; ++k) {
-    s.shift = k * s.bits;
-    s.key_in = k ? w.key[cur ^ 1] : nullptr;
-    s.pos_in = k ? w.pos[cur ^ 1] : nullptr;
-    s.key_out = w.key[cur];
-    s.pos_out = w.pos[cur];
-    if ((rc = launch(sort_count_kernel, dim3(s.tiles), dim3(kSortThreads), 0, st, false, 1, s))) return rc;
-    if ((rc = launch(sort_scan_kernel, dim3(1u << s.bits), dim3(kSortThreads), 0, st, false, 1, s))) return rc;
-    if ((rc = launch(sort_scatter_kernel, dim3(s.tiles), dim3(kSortThreads), 0, st, false, 1, s))) return rc;
-    cur ^= 1;
-  }
   GradParams r{};
-  r.key = w.key[cur ^ 1];
-  r.pos = w.pos[cur ^ 1];
   r.n = s.n;
   r.V = s.V;
   r.tiles = s.tiles;
@@ -282,26 +326,76 @@ int embedding_bwd(const int32_t* ids, int64_t n, const void* g, int g_dtype, int
   r.partial = w.partial;
   r.out = out;
   r.dense = dense ? 1 : 0;
-  if ((rc = launch(grad_heads_kernel, dim3(r.tiles), dim3(kSortThreads), 0, st, false, 1, r))) return rc;
-  if ((rc = launch(grad_number_kernel, dim3(r.tiles), dim3(kSortThreads), 0, st, false, 1, r))) return rc;
-  const int64_t items = (n + kGradPiece - 1) / kGradPiece * r.chunks;
-  if (items > int64_t(INT32_MAX) * 8) return NGRAM_ERR_UNSUPPORTED;
+  int rc;
+  if (cluster) {
+    s.key_out = w.key[0];
+    s.pos_out = w.pos[0];
+    r.key = w.key[0];
+    r.pos = w.pos[0];
+    const ClusterSortParams a{s, passes, r};
+    static std::atomic<uint64_t> done{0};
+    if ((rc = opt_in_smem(sort_cluster_kernel, sizeof(ClusterSmem), done, true))) return rc;
+    int ctas = 1;
+    while (static_cast<int64_t>(ctas) * kClusterItems < n) ctas *= 2;
+    if ((rc = launch(sort_cluster_kernel, dim3(static_cast<unsigned>(ctas)), dim3(kClusterThreads), sizeof(ClusterSmem), st,
+                     false, ctas, a)))
+      return rc;
+  } else {
+    int cur = 0;
+    for (int k = 0; k < passes; ++k) {
+      s.shift = k * s.bits;
+      s.key_in = k ? w.key[cur ^ 1] : nullptr;
+      s.pos_in = k ? w.pos[cur ^ 1] : nullptr;
+      s.key_out = w.key[cur];
+      s.pos_out = w.pos[cur];
+      if ((rc = launch(sort_count_kernel, dim3(s.tiles), dim3(kSortThreads), 0, st, false, 1, s))) return rc;
+      if ((rc = launch(sort_scan_kernel, dim3(1u << s.bits), dim3(kSortThreads), 0, st, false, 1, s))) return rc;
+      if ((rc = launch(sort_scatter_kernel, dim3(s.tiles), dim3(kSortThreads), 0, st, false, 1, s))) return rc;
+      cur ^= 1;
+    }
+    r.key = w.key[cur ^ 1];
+    r.pos = w.pos[cur ^ 1];
+    if ((rc = launch(grad_heads_kernel, dim3(r.tiles), dim3(kSortThreads), 0, st, false, 1, r))) return rc;
+    if ((rc = launch(grad_number_kernel, dim3(r.tiles), dim3(kSortThreads), 0, st, false, 1, r))) return rc;
+  }
+  const int64_t pieces = (n + kGradPiece - 1) / kGradPiece;
+  const int64_t items = pieces * r.chunks, join_items = pieces * ((D + 127) / 128);
+  if (join_items > int64_t(INT32_MAX) * 8) return NGRAM_ERR_UNSUPPORTED;
   const dim3 grid(static_cast<unsigned>((items + 7) / 8));
   rc = g_dtype == NGRAM_BF16 ? launch(grad_reduce_kernel<uint16_t>, grid, dim3(256), 0, st, false, 1, r)
                              : launch(grad_reduce_kernel<float>, grid, dim3(256), 0, st, false, 1, r);
   if (rc) return rc;
-  return launch(grad_join_kernel, grid, dim3(256), 0, st, false, 1, r);
+  return launch(grad_join_kernel, dim3(static_cast<unsigned>((join_items + 7) / 8)), dim3(256), 0, st, false, 1, r);
 }
 
+dim3 row_map_grid(const RowMap& m) { return dim3((m.items + 7) / 8); }
+
+template <int TABLE, typename OutT>
+int launch_lookup(LookupParams& p, uint32_t rows, uint32_t vecs, cudaStream_t st) {
+  const int U = RowMap::unroll(vecs);
+  p.map.set(rows, vecs, U);
+  const dim3 grid = row_map_grid(p.map);
+  if (U == 4) return launch(lookup_kernel<TABLE, OutT, 4>, grid, dim3(256), 0, st, false, 1, p);
+  if (U == 2) return launch(lookup_kernel<TABLE, OutT, 2>, grid, dim3(256), 0, st, false, 1, p);
+  return launch(lookup_kernel<TABLE, OutT, 1>, grid, dim3(256), 0, st, false, 1, p);
+}
 template <int TABLE>
-int launch_lookup(const LookupParams& p, int out_dtype, cudaStream_t st) {
-  constexpr uint32_t per_block = 256 * kLookupUnroll;
-  const dim3 grid((p.vecs + per_block - 1) / per_block);
-  return out_dtype == NGRAM_BF16 ? launch(lookup_kernel<TABLE, uint16_t>, grid, dim3(256), 0, st, false, 1, p)
-                                 : launch(lookup_kernel<TABLE, float>, grid, dim3(256), 0, st, false, 1, p);
+int launch_lookup_to(LookupParams& p, int out_dtype, uint32_t rows, uint32_t vecs, cudaStream_t st) {
+  return out_dtype == NGRAM_BF16 ? launch_lookup<TABLE, uint16_t>(p, rows, vecs, st)
+                                 : launch_lookup<TABLE, float>(p, rows, vecs, st);
 }
 
-// Rows a launch numbers in 32 bits: at most 2^30 vectors of eight elements.
+template <typename T, bool VEC>
+int launch_quantize(Mx4QuantParams& p, uint32_t rows, uint32_t vecs, cudaStream_t st) {
+  const int U = RowMap::unroll(vecs);
+  p.map.set(rows, vecs, U);
+  const dim3 grid = row_map_grid(p.map);
+  if (U == 4) return launch(mx4_quantize_kernel<T, VEC, 4>, grid, dim3(256), 0, st, false, 1, p);
+  if (U == 2) return launch(mx4_quantize_kernel<T, VEC, 2>, grid, dim3(256), 0, st, false, 1, p);
+  return launch(mx4_quantize_kernel<T, VEC, 1>, grid, dim3(256), 0, st, false, 1, p);
+}
+
+// Rows of a launch whose warps are numbered in 32 bits: at most 2^30 vectors of eight elements.
 int64_t rows_per_launch(int64_t cols) {
   const int64_t r = (int64_t(1) << 30) / (cols / 8);
   return r < 1 ? 1 : r;
@@ -336,24 +430,19 @@ int ngram_mx4_quantize(const void* src, int dtype, int64_t rows, int64_t cols, i
     Mx4QuantParams p{};
     p.src = static_cast<const uint8_t*>(src) + r0 * src_stride * elt;
     p.src_stride = src_stride;
-    p.vecs = static_cast<uint32_t>(r * (cols / 8));
-    p.per_row.set(static_cast<uint32_t>(cols / 8));
     p.row0 = r0;
     p.cols = static_cast<int>(cols);
     p.kt = static_cast<int>((cols + 127) / 128);
     p.codes = static_cast<uint8_t*>(codes) + r0 * (cols / 2);
     p.tiles = layout == NGRAM_MX4_TILES ? 1 : 0;
     p.scales = static_cast<uint8_t*>(scales) + (p.tiles ? 0 : r0 * (cols / kMxBlock));
-    constexpr uint32_t per_block = 256 * kMx4QuantUnroll;
-    const dim3 grid((p.vecs + per_block - 1) / per_block);
+    const uint32_t n = static_cast<uint32_t>(r), vecs = static_cast<uint32_t>(cols / 8);
     const cudaStream_t st = static_cast<cudaStream_t>(stream);
     int rc;
     if (dtype == NGRAM_BF16)
-      rc = vec ? launch(mx4_quantize_kernel<uint16_t, true>, grid, dim3(256), 0, st, false, 1, p)
-               : launch(mx4_quantize_kernel<uint16_t, false>, grid, dim3(256), 0, st, false, 1, p);
+      rc = vec ? launch_quantize<uint16_t, true>(p, n, vecs, st) : launch_quantize<uint16_t, false>(p, n, vecs, st);
     else
-      rc = vec ? launch(mx4_quantize_kernel<float, true>, grid, dim3(256), 0, st, false, 1, p)
-               : launch(mx4_quantize_kernel<float, false>, grid, dim3(256), 0, st, false, 1, p);
+      rc = vec ? launch_quantize<float, true>(p, n, vecs, st) : launch_quantize<float, false>(p, n, vecs, st);
     if (rc) return rc;
   }
   return NGRAM_OK;
@@ -382,20 +471,20 @@ int ngram_mx4_product(const ngram_mx4* A, const ngram_mx4* B, int64_t M, int64_t
   const DeviceScope dev(workspace);
   if (dev.rc) return dev.rc;
   Mx4GemmParams prm{};
-  prm.sa = static_cast<const uint8_t*>(A->scales);
-  prm.sb = static_cast<const uint8_t*>(B->scales);
   prm.M = static_cast<int>(M);
   prm.N = static_cast<int>(N);
   prm.K = static_cast<int>(K);
   prm.scale = alpha;
   prm.out = out;
   prm.ldo = out_stride;
-  prm.vec = aligned16(out) && out_stride * elt % 16 == 0 ? 1 : 0;
+  prm.vec16 = aligned16(out) && out_stride * elt % 16 == 0 ? 1 : 0;
+  prm.vec32 = aligned32(out) && out_stride * elt % 32 == 0 ? 1 : 0;
   prm.status = status_ptr(workspace);
-  const auto *Ac = static_cast<const uint8_t*>(A->codes), *Bc = static_cast<const uint8_t*>(B->codes);
+  const Mx4Operands o{static_cast<const uint8_t*>(A->codes), static_cast<const uint8_t*>(A->scales),
+                      static_cast<const uint8_t*>(B->codes), static_cast<const uint8_t*>(B->scales)};
   const cudaStream_t st = static_cast<cudaStream_t>(stream);
-  return out_dtype == NGRAM_F32 ? launch_mx4_gemm<float>(prm, Ac, Bc, device_sms(), st)
-                                : launch_mx4_gemm<uint16_t>(prm, Ac, Bc, device_sms(), st);
+  return out_dtype == NGRAM_F32 ? launch_mx4_gemm<float>(prm, o, device_sms(), st)
+                                : launch_mx4_gemm<uint16_t>(prm, o, device_sms(), st);
 }
 
 size_t ngram_embed_mx4_workspace_bytes(const ngram_embed_plan* plan, int64_t max_tokens) {
@@ -472,8 +561,6 @@ int ngram_embedding_fwd(const void* table, const void* table_scales, int table_d
     p.ids = ids ? ids + r0 : nullptr;
     p.V = static_cast<uint32_t>(V);
     p.pad_id = pad_id;
-    p.per_row.set(static_cast<uint32_t>(D / 8));
-    p.vecs = static_cast<uint32_t>(r * (D / 8));
     p.scale = scale;
     p.out = static_cast<uint8_t*>(out) + r0 * out_stride * elt;
     p.out_stride = out_stride;
@@ -481,9 +568,10 @@ int ngram_embedding_fwd(const void* table, const void* table_scales, int table_d
     p.status = status_ptr(workspace);
     const cudaStream_t st = static_cast<cudaStream_t>(stream);
     int rc;
-    if (table_dtype == NGRAM_BF16) rc = launch_lookup<kTableBf16>(p, out_dtype, st);
-    else if (table_dtype == NGRAM_F32) rc = launch_lookup<kTableF32>(p, out_dtype, st);
-    else rc = launch_lookup<kTableMx4>(p, out_dtype, st);
+    const uint32_t rows = static_cast<uint32_t>(r), vecs = static_cast<uint32_t>(D / 8);
+    if (table_dtype == NGRAM_BF16) rc = launch_lookup_to<kTableBf16>(p, out_dtype, rows, vecs, st);
+    else if (table_dtype == NGRAM_F32) rc = launch_lookup_to<kTableF32>(p, out_dtype, rows, vecs, st);
+    else rc = launch_lookup_to<kTableMx4>(p, out_dtype, rows, vecs, st);
     if (rc) return rc;
   }
   return NGRAM_OK;

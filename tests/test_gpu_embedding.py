@@ -108,6 +108,8 @@ def check_rows(ne, ids, g, V, scale, pad, ws=None):
     (64, 40, 256, "same"), (65, 40, 256, "same"), (257, 255, 136, "uniform"), (1024, 256, 24, "zipf"),
     (1025, 257, 8, "zipf"), (1500, 100000, 512, "distinct"), (3000, 70000, 72, "zipf"), (5000, 1 << 24, 8, "uniform"),
     (7001, 50, 32, "uniform"), (20000, 131072, 16, "zipf"),
+    (4096, 300, 8, "zipf"), (4097, 2000, 8, "uniform"), (65536, 131072, 8, "zipf"),  # one cluster sorts up to 65536
+    (65537, 131071, 8, "zipf"), (70001, 1 << 22, 8, "uniform"), (100003, 200, 16, "uniform"),
 ])
 def test_gradient_rows_and_dense(ne, n, V, D, kind, dtype):
     rng = np.random.default_rng(n + V)
