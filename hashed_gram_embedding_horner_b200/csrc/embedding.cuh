@@ -7,8 +7,8 @@
 // Gradient: dTable[v] = scale * sum_{i : ids[i] = v} g_i. The positions are sorted by id with
 // a stable radix sort; runs of equal ids are summed in fp32 by whoever owns them, without
 // atomics, so the sum's order, and its bits, depend on the ids alone:
-//   - the sorted positions are cut into pieces of kGradPiece; a warp sums the rows of a piece
-//     for 256 columns, in ascending position order;
+//   - the sorted positions are cut into pieces (of 128, 32 or 8: the longest that fill the GPU);
+//     a warp sums the rows of a piece for 256 columns, in ascending position order;
 //   - a run inside one piece is written out by that warp; a run that crosses a piece's border
 //     leaves one partial sum in each piece it touches, which a second kernel adds in piece
 //     order.
@@ -311,7 +311,6 @@ __global__ void __launch_bounds__(kSortThreads) sort_scatter_kernel(const __grid
 
 // ------------------------------------------------------------------ sums over sorted runs
 
-constexpr int kGradPiece = 32;
 
 struct GradParams {
   const uint32_t* key;    // [n] sorted; padded positions (key V) last
@@ -320,7 +319,8 @@ struct GradParams {
   uint32_t V;
   uint32_t tiles;         // of kSortTile sorted positions
   uint32_t* tile_heads;   // [tiles]: first positions of runs in each tile
-  int32_t* piece_run;     // [ceil(n / kGradPiece)]: the run (unique id) a piece begins in
+  uint32_t piece;         // positions a piece
+  int32_t* piece_run;     // [ceil(n / piece)]: the run (unique id) a piece begins in
   int32_t* rows_out;      // compact form: the unique ids
   int32_t* count_out;
   const void* g;          // [n x D], row stride g_stride elements
@@ -370,7 +370,7 @@ __global__ void __launch_bounds__(kSortThreads) grad_number_kernel(const __grid_
       if (p.rows_out) p.rows_out[run] = static_cast<int32_t>(p.key[i]);
       ++run;
     }
-    if (i < p.n && i % kGradPiece == 0) p.piece_run[i / kGradPiece] = static_cast<int32_t>(run) - 1;
+    if (i < p.n && i % p.piece == 0) p.piece_run[i / p.piece] = static_cast<int32_t>(run) - 1;
   }
   if (p.count_out && blockIdx.x + 1 == p.tiles && threadIdx.x == 0) *p.count_out = static_cast<int32_t>(base + total);
 }
@@ -418,28 +418,21 @@ __device__ __forceinline__ float4* grad_partial(const GradParams& p, uint32_t pi
 // One warp a (piece, 256 columns), eight columns a lane, kGradLoads rows in flight.
 constexpr int kGradLoads = 8;
 
-template <typename T>
+template <typename T, int PIECE>
 __global__ void __launch_bounds__(256) grad_reduce_kernel(const __grid_constant__ GradParams p) {
+  constexpr int kLanes = PIECE < 32 ? PIECE : 32;  // sorted positions a lane holds one of at a time
   const uint64_t item = static_cast<uint64_t>(blockIdx.x) * 8 + (threadIdx.x >> 5);
   const int lane = threadIdx.x & 31;
   const uint32_t piece = static_cast<uint32_t>(item / p.chunks);
   const int c = static_cast<int>(item - static_cast<uint64_t>(piece) * p.chunks) * 256 + lane * 8;
-  const uint32_t k0 = piece * kGradPiece;
-  if (k0 >= p.n) return;
-  // this lane's sorted position of the piece
-  const uint32_t i = k0 + lane;
-  const uint32_t key = i < p.n ? p.key[i] : p.V;
-  const int32_t pos = i < p.n ? p.pos[i] : 0;
-  const int len = __popc(__ballot_sync(0xffffffffu, key < p.V));  // padded positions are last
-  if (len == 0) return;
+  const uint32_t begin = piece * PIECE;
+  if (begin >= p.n || p.key[begin] >= p.V) return;  // padded positions are last
   const bool on = c < p.D;  // lanes past the last column only carry their position
-  const uint32_t first = __shfl_sync(0xffffffffu, key, 0), last = __shfl_sync(0xffffffffu, key, len - 1);
-  const bool from_before = k0 > 0 && p.key[k0 - 1] == first;
-  const bool to_after = len == kGradPiece && k0 + kGradPiece < p.n && p.key[k0 + kGradPiece] == last;
   int32_t run = p.piece_run[piece];
+  uint32_t cur = p.key[begin];
+  bool open = begin > 0 && p.key[begin - 1] == cur;  // the current run began in an earlier piece
   const T* g = static_cast<const T*>(p.g) + c;
   float acc[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-  bool open = from_before;  // the current run began in an earlier piece
   auto finish = [&](uint32_t id) {
     if (on) grad_finish(p, run, id, c, acc);
   };
@@ -449,31 +442,40 @@ __global__ void __launch_bounds__(256) grad_reduce_kernel(const __grid_constant_
     dst[0] = make_float4(acc[0], acc[1], acc[2], acc[3]);
     dst[1] = make_float4(acc[4], acc[5], acc[6], acc[7]);
   };
-  uint32_t cur = first;
+  int len = kLanes;
 #pragma unroll 1
-  for (int r0 = 0; r0 < len; r0 += kGradLoads) {
-    uint4 rows[kGradLoads][sizeof(T) / 2];
+  for (int part = 0; part < PIECE / kLanes && len == kLanes; ++part) {
+    const uint32_t i = begin + part * kLanes + lane;
+    const bool mine = lane < kLanes && i < p.n;
+    const uint32_t key = mine ? p.key[i] : p.V;
+    const int32_t pos = mine ? p.pos[i] : 0;
+    len = __popc(__ballot_sync(0xffffffffu, key < p.V));
+#pragma unroll 1
+    for (int r0 = 0; r0 < len; r0 += kGradLoads) {
+      uint4 rows[kGradLoads][sizeof(T) / 2];
 #pragma unroll
-    for (int r = 0; r < kGradLoads; ++r) {
-      const int32_t at = __shfl_sync(0xffffffffu, pos, (r0 + r) & 31);
-      if (on && r0 + r < len) grad_load8<T>(g + static_cast<int64_t>(at) * p.g_stride, rows[r]);
-    }
-#pragma unroll
-    for (int r = 0; r < kGradLoads; ++r) {
-      const uint32_t kr = __shfl_sync(0xffffffffu, key, (r0 + r) & 31);
-      if (r0 + r >= len) continue;
-      if (kr != cur) {
-        if (open) leave(0); else finish(cur);
-        open = false;
-#pragma unroll
-        for (int j = 0; j < 8; ++j) acc[j] = 0.f;
-        cur = kr;
-        ++run;
+      for (int r = 0; r < kGradLoads; ++r) {
+        const int32_t at = __shfl_sync(0xffffffffu, pos, (r0 + r) & 31);
+        if (on && r0 + r < len) grad_load8<T>(g + static_cast<int64_t>(at) * p.g_stride, rows[r]);
       }
-      grad_add8<T>(rows[r], acc);
+#pragma unroll
+      for (int r = 0; r < kGradLoads; ++r) {
+        const uint32_t kr = __shfl_sync(0xffffffffu, key, (r0 + r) & 31);
+        if (r0 + r >= len) continue;
+        if (kr != cur) {
+          if (open) leave(0); else finish(cur);
+          open = false;
+#pragma unroll
+          for (int j = 0; j < 8; ++j) acc[j] = 0.f;
+          cur = kr;
+          ++run;
+        }
+        grad_add8<T>(rows[r], acc);
+      }
     }
   }
-  if (to_after) leave(open ? 0 : 1);
+  const uint64_t end = static_cast<uint64_t>(begin) + PIECE;
+  if (end < p.n && p.key[end] == cur) leave(open ? 0 : 1);  // it goes on in the next piece
   else if (open) leave(0);
   else finish(cur);
 }
@@ -482,27 +484,28 @@ __global__ void __launch_bounds__(256) grad_reduce_kernel(const __grid_constant_
 // columns) adds the partial sums in piece order, kJoinLoads of them in flight: a frequent id's
 // run is hundreds of pieces long, and a warp alone waits for every load (4 in flight: 48 us for
 // 32768 Zipf ids at D = 4096).
-constexpr int kJoinLoads = 16;
+constexpr int kJoinLoads = 8;
 
-__global__ void __launch_bounds__(256) grad_join_kernel(const __grid_constant__ GradParams p) {
+__global__ void __launch_bounds__(256, 4) grad_join_kernel(const __grid_constant__ GradParams p) {
   const int chunks = (p.D + 127) / 128;
   const uint64_t item = static_cast<uint64_t>(blockIdx.x) * 8 + (threadIdx.x >> 5);
   const int lane = threadIdx.x & 31;
   const uint32_t piece = static_cast<uint32_t>(item / chunks);
   const int c = static_cast<int>(item - static_cast<uint64_t>(piece) * chunks) * 128 + lane * 4;
-  const uint64_t k0 = static_cast<uint64_t>(piece) * kGradPiece, k1 = k0 + kGradPiece;
+  const uint64_t k0 = static_cast<uint64_t>(piece) * p.piece, k1 = k0 + p.piece;
   if (k1 >= p.n) return;
   const uint32_t key = p.key[k1 - 1];
   if (key >= p.V || p.key[k1] != key) return;
   if (p.key[k0] == key && k0 > 0 && p.key[k0 - 1] == key) return;  // it began earlier
-  if (c >= p.D) return;
-  // the run's last position: pieces up to the one that holds it
-  uint32_t lo = static_cast<uint32_t>(k1), hi = p.n;  // key[lo] == key, key[hi] beyond
-  while (hi - lo > 1) {
-    const uint32_t mid = lo + (hi - lo) / 2;
-    if (p.key[mid] == key) lo = mid; else hi = mid;
+  // the run's last piece: the pieces that begin with its id, 32 at a time, a lane each
+  uint32_t last = piece;
+  for (bool more = true; more;) {
+    const uint64_t at = (static_cast<uint64_t>(last) + 1 + lane) * p.piece;
+    const unsigned in = __ballot_sync(0xffffffffu, at < p.n && p.key[at] == key);
+    more = in == 0xffffffffu;
+    last += more ? 32 : __ffs(~in) - 1;
   }
-  const uint32_t last = lo / kGradPiece;
+  if (c >= p.D) return;
   auto partial = [&](uint32_t q, int which) {
     return reinterpret_cast<const float4*>(p.partial + (static_cast<size_t>(q) * 2 + which) * p.D + c);
   };
@@ -535,21 +538,21 @@ __global__ void __launch_bounds__(256) grad_join_kernel(const __grid_constant__ 
 // ------------------------------------------------------------------ sort in one cluster
 //
 // Up to kClusterMax positions are sorted and their runs numbered in one launch, by a cluster of
-// CTAs that hold all of them in shared memory: each CTA ranks its kClusterItems positions by
-// digit, the CTAs exchange their digit counts, and every position is stored straight into its
+// CTAs that hold all of them in shared memory: each CTA ranks its positions by digit, the CTAs exchange their digit counts, and every position is stored straight into its
 // place in the shared memory of the CTA that the place belongs to. Positions past n carry the
 // largest key, so they stay last. Measured for 32768 ids below 131072: 13 us, against 45 us of
 // launches and gaps for the tiled sort and the numbering kernels.
 
 constexpr int kClusterThreads = 1024;
-constexpr int kClusterItems = 4096;  // of one CTA: four a thread
+constexpr int kClusterMaxItems = 4;  // positions a thread: 1, 2 or 4, as few as hold n
 constexpr int kClusterCtas = 16;
-constexpr int kClusterMax = kClusterItems * kClusterCtas;
+constexpr int kClusterMax = kClusterThreads * kClusterMaxItems * kClusterCtas;
 constexpr int kClusterMaxBits = 9;
 
+template <int ITEMS>
 struct ClusterSmem {
-  uint32_t key[kClusterItems];
-  int32_t pos[kClusterItems];
+  uint32_t key[kClusterThreads * ITEMS];
+  int32_t pos[kClusterThreads * ITEMS];
   uint16_t warp_count[kClusterThreads / 32][1 << kClusterMaxBits];
   uint32_t count[kClusterCtas][1 << kClusterMaxBits];  // of every CTA, pushed by it
   uint32_t start[1 << kClusterMaxBits];
@@ -602,31 +605,34 @@ __device__ __forceinline__ uint32_t cluster_block_scan(uint32_t x, uint32_t* war
   return __shfl_sync(0xffffffffu, p - ws, w) + s - x;
 }
 
+template <int ITEMS>
 __global__ void __launch_bounds__(kClusterThreads, 1) sort_cluster_kernel(const __grid_constant__ ClusterSortParams a) {
+  constexpr uint32_t kItems = kClusterThreads * ITEMS;  // of one CTA
+  constexpr int kWarpItems = 32 * ITEMS;
   extern __shared__ __align__(16) uint8_t cluster_raw[];
-  ClusterSmem& m = *reinterpret_cast<ClusterSmem*>(cluster_raw);
+  auto& m = *reinterpret_cast<ClusterSmem<ITEMS>*>(cluster_raw);
   const SortParams& p = a.s;
   const int tid = threadIdx.x, lane = tid & 31, w = tid >> 5;
   const uint32_t rank = cluster_ctarank(), ctas = gridDim.x;
   const int bins = 1 << p.bits;
-  const uint32_t base = rank * kClusterItems;
+  const uint32_t base = rank * kItems;
   constexpr uint32_t kLast = 0xFFFFFFFFu;
-  uint32_t key[4];
-  int32_t pos[4];
+  uint32_t key[ITEMS];
+  int32_t pos[ITEMS];
 #pragma unroll
-  for (int j = 0; j < 4; ++j) {
-    const uint32_t i = base + w * 128 + j * 32 + lane;
+  for (int j = 0; j < ITEMS; ++j) {
+    const uint32_t i = base + w * kWarpItems + j * 32 + lane;
     key[j] = i < p.n ? sort_key(p, i, true) : kLast;
     pos[j] = static_cast<int32_t>(i);
   }
   cluster_barrier(ctas);  // every CTA runs before its shared memory is written
   for (int pass = 0; pass < a.passes; ++pass) {
     const int shift = pass * p.bits;
-    uint32_t rk[4];
+    uint32_t rk[ITEMS];
     for (int b = lane; b < bins; b += 32) m.warp_count[w][b] = 0;
     __syncwarp();
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
+    for (int j = 0; j < ITEMS; ++j) {
       const uint32_t dg = (key[j] >> shift) & (bins - 1);
       const uint32_t peers = __match_any_sync(0xffffffffu, dg);
       const uint32_t before = m.warp_count[w][dg];
@@ -659,29 +665,29 @@ __global__ void __launch_bounds__(kClusterThreads, 1) sort_cluster_kernel(const 
     if (tid < bins) m.start[tid] = smaller + lower;
     __syncthreads();
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
+    for (int j = 0; j < ITEMS; ++j) {
       const uint32_t dg = (key[j] >> shift) & (bins - 1);
       const uint32_t at = m.start[dg] + m.warp_count[w][dg] + rk[j];
-      const uint32_t cta = at / kClusterItems, in = at % kClusterItems;
+      const uint32_t cta = at / kItems, in = at % kItems;
       st_cluster_u32(map_to_cta(smem_u32(&m.key[in]), cta), key[j]);
       st_cluster_u32(map_to_cta(smem_u32(&m.pos[in]), cta), static_cast<uint32_t>(pos[j]));
     }
     cluster_barrier(ctas);
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      key[j] = m.key[w * 128 + j * 32 + lane];
-      pos[j] = m.pos[w * 128 + j * 32 + lane];
+    for (int j = 0; j < ITEMS; ++j) {
+      key[j] = m.key[w * kWarpItems + j * 32 + lane];
+      pos[j] = m.pos[w * kWarpItems + j * 32 + lane];
     }
   }
-  // sorted: out, and the runs numbered, four neighbouring positions a thread
-  const uint32_t l0 = tid * 4;
+  // sorted: out, and the runs numbered, ITEMS neighbouring positions a thread
+  const uint32_t l0 = tid * ITEMS;
   uint32_t prev = l0 > 0 ? m.key[l0 - 1] : kLast;
   const bool first = rank == 0 && tid == 0;
-  if (tid == 0 && rank > 0) prev = ld_cluster_u32(map_to_cta(smem_u32(&m.key[kClusterItems - 1]), rank - 1));
-  bool head[4];
-  uint32_t mine = 0, k4[4];
+  if (tid == 0 && rank > 0) prev = ld_cluster_u32(map_to_cta(smem_u32(&m.key[kItems - 1]), rank - 1));
+  bool head[ITEMS];
+  uint32_t mine = 0, k4[ITEMS];
 #pragma unroll
-  for (int j = 0; j < 4; ++j) {
+  for (int j = 0; j < ITEMS; ++j) {
     k4[j] = m.key[l0 + j];
     head[j] = base + l0 + j < p.n && k4[j] < p.V && ((first && j == 0) || k4[j] != prev);
     prev = k4[j];
@@ -701,13 +707,13 @@ __global__ void __launch_bounds__(kClusterThreads, 1) sort_cluster_kernel(const 
     all += m.heads[r];
   }
 #pragma unroll
-  for (int j = 0; j < 4; ++j) {
+  for (int j = 0; j < ITEMS; ++j) {
     const uint32_t i = base + l0 + j;
     if (head[j]) {
       if (a.r.rows_out) a.r.rows_out[run] = static_cast<int32_t>(k4[j]);
       ++run;
     }
-    if (i < p.n && i % kGradPiece == 0) a.r.piece_run[i / kGradPiece] = static_cast<int32_t>(run) - 1;
+    if (i < p.n && i % a.r.piece == 0) a.r.piece_run[i / a.r.piece] = static_cast<int32_t>(run) - 1;
   }
   if (a.r.count_out && first) *a.r.count_out = static_cast<int32_t>(all);
 }

@@ -245,6 +245,33 @@ struct GradWs {
   float* partial;
   size_t bytes;
 };
+// Positions a piece: the longest of 128, 32 and 8 that leaves kGradWarps warps. Long pieces leave
+// few partial sums of the frequent ids to join (32768 Zipf ids at D = 4096, pieces of 16 / 32 /
+// 128: 44 / 22 / JOIN us for the join); short ones have their row loads in flight at once where
+// the warps are few (641 ids of 136 columns, pieces of 32 / 8: 16 / 6 us for the sums).
+constexpr int64_t kGradWarps = 4096;
+constexpr int kGradPieces[3] = {128, 32, 8};
+int64_t grad_warps(int64_t n, int64_t D, int piece) { return (n + piece - 1) / piece * ((D + 255) / 256); }
+int grad_piece(int64_t n, int64_t D) {
+  for (int k = 0; k < 2; ++k)
+    if (grad_warps(n, D, kGradPieces[k]) >= kGradWarps) return kGradPieces[k];
+  return kGradPieces[2];
+}
+// The most pieces that a call of up to n positions takes (fewer positions may take shorter ones,
+// never more than kGradWarps warps of them).
+int64_t grad_max_pieces(int64_t n, int64_t D) {
+  const int64_t chunks = (D + 255) / 256;
+  int64_t most = (n + kGradPieces[0] - 1) / kGradPieces[0];
+  for (int k = 1; k < 3; ++k) {
+    // pieces of this length: only while the next longer ones are fewer than kGradWarps warps
+    const int64_t longer = kGradPieces[k - 1], limit = (kGradWarps + chunks - 1) / chunks * longer;
+    const int64_t m = ((n < limit ? n : limit) + kGradPieces[k] - 1) / kGradPieces[k];
+    if (m > most) most = m;
+  }
+  return most;
+}
+
+// Sized for every call of up to n positions.
 GradWs grad_ws(int64_t n, int64_t D, void* ws) {
   GradWs w{};
   size_t off = kHeadBytes;
@@ -254,7 +281,8 @@ GradWs grad_ws(int64_t n, int64_t D, void* ws) {
     return at;
   };
   const size_t N = static_cast<size_t>(n);
-  const size_t tiles = (N + kSortTile - 1) / kSortTile, pieces = (N + kGradPiece - 1) / kGradPiece;
+  const size_t tiles = (N + kSortTile - 1) / kSortTile;
+  const size_t pieces = static_cast<size_t>(grad_max_pieces(n, D));
   const size_t k0 = take(N * 4), k1 = take(N * 4), p0 = take(N * 4), p1 = take(N * 4);
   const size_t cn = take(tiles << (kSortMaxBits + 2)), to = take(4u << kSortMaxBits), th = take(tiles * 4);
   const size_t pr = take(pieces * 4), pa = take(pieces * 2 * static_cast<size_t>(D) * 4);
@@ -272,6 +300,25 @@ GradWs grad_ws(int64_t n, int64_t D, void* ws) {
     w.partial = reinterpret_cast<float*>(b + pa);
   }
   return w;
+}
+
+template <int ITEMS>
+int launch_cluster_sort(const ClusterSortParams& a, int64_t n, cudaStream_t st) {
+  static std::atomic<uint64_t> done{0};
+  constexpr int bytes = sizeof(ClusterSmem<ITEMS>);
+  const int rc = opt_in_smem(sort_cluster_kernel<ITEMS>, bytes, done, true);
+  if (rc) return rc;
+  int ctas = 1;
+  while (static_cast<int64_t>(ctas) * kClusterThreads * ITEMS < n) ctas *= 2;
+  return launch(sort_cluster_kernel<ITEMS>, dim3(static_cast<unsigned>(ctas)), dim3(kClusterThreads), bytes, st, false, ctas,
+                a);
+}
+
+template <typename T>
+int launch_grad_reduce(const GradParams& r, dim3 grid, cudaStream_t st) {
+  if (r.piece == 128) return launch(grad_reduce_kernel<T, 128>, grid, dim3(256), 0, st, false, 1, r);
+  if (r.piece == 32) return launch(grad_reduce_kernel<T, 32>, grid, dim3(256), 0, st, false, 1, r);
+  return launch(grad_reduce_kernel<T, 8>, grid, dim3(256), 0, st, false, 1, r);
 }
 
 int embedding_bwd(const int32_t* ids, int64_t n, const void* g, int g_dtype, int64_t g_stride, int64_t V, int64_t D,
@@ -315,6 +362,7 @@ int embedding_bwd(const int32_t* ids, int64_t n, const void* g, int g_dtype, int
   r.V = s.V;
   r.tiles = s.tiles;
   r.tile_heads = w.tile_heads;
+  r.piece = static_cast<uint32_t>(grad_piece(n, D));
   r.piece_run = w.piece_run;
   r.rows_out = rows_out;
   r.count_out = count_out;
@@ -333,13 +381,10 @@ int embedding_bwd(const int32_t* ids, int64_t n, const void* g, int g_dtype, int
     r.key = w.key[0];
     r.pos = w.pos[0];
     const ClusterSortParams a{s, passes, r};
-    static std::atomic<uint64_t> done{0};
-    if ((rc = opt_in_smem(sort_cluster_kernel, sizeof(ClusterSmem), done, true))) return rc;
-    int ctas = 1;
-    while (static_cast<int64_t>(ctas) * kClusterItems < n) ctas *= 2;
-    if ((rc = launch(sort_cluster_kernel, dim3(static_cast<unsigned>(ctas)), dim3(kClusterThreads), sizeof(ClusterSmem), st,
-                     false, ctas, a)))
-      return rc;
+    const int64_t per = int64_t(kClusterThreads) * kClusterCtas;
+    rc = n <= per ? launch_cluster_sort<1>(a, n, st) : (n <= 2 * per ? launch_cluster_sort<2>(a, n, st)
+                                                                    : launch_cluster_sort<4>(a, n, st));
+    if (rc) return rc;
   } else {
     int cur = 0;
     for (int k = 0; k < passes; ++k) {
@@ -358,12 +403,11 @@ int embedding_bwd(const int32_t* ids, int64_t n, const void* g, int g_dtype, int
     if ((rc = launch(grad_heads_kernel, dim3(r.tiles), dim3(kSortThreads), 0, st, false, 1, r))) return rc;
     if ((rc = launch(grad_number_kernel, dim3(r.tiles), dim3(kSortThreads), 0, st, false, 1, r))) return rc;
   }
-  const int64_t pieces = (n + kGradPiece - 1) / kGradPiece;
+  const int64_t pieces = (n + r.piece - 1) / r.piece;
   const int64_t items = pieces * r.chunks, join_items = pieces * ((D + 127) / 128);
   if (join_items > int64_t(INT32_MAX) * 8) return NGRAM_ERR_UNSUPPORTED;
   const dim3 grid(static_cast<unsigned>((items + 7) / 8));
-  rc = g_dtype == NGRAM_BF16 ? launch(grad_reduce_kernel<uint16_t>, grid, dim3(256), 0, st, false, 1, r)
-                             : launch(grad_reduce_kernel<float>, grid, dim3(256), 0, st, false, 1, r);
+  rc = g_dtype == NGRAM_BF16 ? launch_grad_reduce<uint16_t>(r, grid, st) : launch_grad_reduce<float>(r, grid, st);
   if (rc) return rc;
   return launch(grad_join_kernel, dim3(static_cast<unsigned>((join_items + 7) / 8)), dim3(256), 0, st, false, 1, r);
 }
