@@ -551,8 +551,7 @@ constexpr int kClusterMaxBits = 9;
 
 template <int ITEMS>
 struct ClusterSmem {
-  uint32_t key[kClusterThreads * ITEMS];
-  int32_t pos[kClusterThreads * ITEMS];
+  uint2 item[kClusterThreads * ITEMS];  // key, position
   uint16_t warp_count[kClusterThreads / 32][1 << kClusterMaxBits];
   uint32_t count[kClusterCtas][1 << kClusterMaxBits];  // of every CTA, pushed by it
   uint32_t start[1 << kClusterMaxBits];
@@ -568,6 +567,20 @@ struct ClusterSortParams {
 
 __device__ __forceinline__ void st_cluster_u32(uint32_t addr, uint32_t v) {
   asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(addr), "r"(v) : "memory");
+}
+__device__ __forceinline__ void st_cluster_v2(uint32_t addr, uint32_t a, uint32_t b) {
+  asm volatile("st.shared::cluster.v2.u32 [%0], {%1, %2};" ::"r"(addr), "r"(a), "r"(b) : "memory");
+}
+// Lanes whose digit equals this lane's: a vote a bit. (__match_any_sync does it in one
+// instruction, at about 2 us an item and pass for the 32 warps of a block.)
+__device__ __forceinline__ uint32_t match_digit(uint32_t dg, int bits) {
+  uint32_t same = 0xffffffffu;
+  for (int b = 0; b < bits; ++b) {
+    const bool on = (dg >> b) & 1u;
+    const uint32_t votes = __ballot_sync(0xffffffffu, on);
+    same &= on ? votes : ~votes;
+  }
+  return same;
 }
 __device__ __forceinline__ uint32_t ld_cluster_u32(uint32_t addr) {
   uint32_t v;
@@ -634,7 +647,7 @@ __global__ void __launch_bounds__(kClusterThreads, 1) sort_cluster_kernel(const 
 #pragma unroll
     for (int j = 0; j < ITEMS; ++j) {
       const uint32_t dg = (key[j] >> shift) & (bins - 1);
-      const uint32_t peers = __match_any_sync(0xffffffffu, dg);
+      const uint32_t peers = match_digit(dg, p.bits);
       const uint32_t before = m.warp_count[w][dg];
       __syncwarp();
       rk[j] = before + __popc(peers & ((1u << lane) - 1u));
@@ -669,32 +682,33 @@ __global__ void __launch_bounds__(kClusterThreads, 1) sort_cluster_kernel(const 
       const uint32_t dg = (key[j] >> shift) & (bins - 1);
       const uint32_t at = m.start[dg] + m.warp_count[w][dg] + rk[j];
       const uint32_t cta = at / kItems, in = at % kItems;
-      st_cluster_u32(map_to_cta(smem_u32(&m.key[in]), cta), key[j]);
-      st_cluster_u32(map_to_cta(smem_u32(&m.pos[in]), cta), static_cast<uint32_t>(pos[j]));
+      st_cluster_v2(map_to_cta(smem_u32(&m.item[in]), cta), key[j], static_cast<uint32_t>(pos[j]));
     }
     cluster_barrier(ctas);
 #pragma unroll
     for (int j = 0; j < ITEMS; ++j) {
-      key[j] = m.key[w * kWarpItems + j * 32 + lane];
-      pos[j] = m.pos[w * kWarpItems + j * 32 + lane];
+      const uint2 x = m.item[w * kWarpItems + j * 32 + lane];
+      key[j] = x.x;
+      pos[j] = static_cast<int32_t>(x.y);
     }
   }
   // sorted: out, and the runs numbered, ITEMS neighbouring positions a thread
   const uint32_t l0 = tid * ITEMS;
-  uint32_t prev = l0 > 0 ? m.key[l0 - 1] : kLast;
+  uint32_t prev = l0 > 0 ? m.item[l0 - 1].x : kLast;
   const bool first = rank == 0 && tid == 0;
-  if (tid == 0 && rank > 0) prev = ld_cluster_u32(map_to_cta(smem_u32(&m.key[kItems - 1]), rank - 1));
+  if (tid == 0 && rank > 0) prev = ld_cluster_u32(map_to_cta(smem_u32(&m.item[kItems - 1].x), rank - 1));
   bool head[ITEMS];
   uint32_t mine = 0, k4[ITEMS];
 #pragma unroll
   for (int j = 0; j < ITEMS; ++j) {
-    k4[j] = m.key[l0 + j];
+    const uint2 x = m.item[l0 + j];
+    k4[j] = x.x;
     head[j] = base + l0 + j < p.n && k4[j] < p.V && ((first && j == 0) || k4[j] != prev);
     prev = k4[j];
     mine += head[j] ? 1u : 0u;
     if (base + l0 + j < p.n) {
       p.key_out[base + l0 + j] = k4[j];
-      p.pos_out[base + l0 + j] = m.pos[l0 + j];
+      p.pos_out[base + l0 + j] = static_cast<int32_t>(x.y);
     }
   }
   uint32_t total;
