@@ -71,15 +71,14 @@ __device__ __forceinline__ void hash_window(const HashParams& p, int64_t i, int6
   }
 }
 
-// Eq. 2 for token i of a sequence starting at `start`, with the sequence's committed
-// history (slot >= 0: hist_len ids, those before hist_from evicted) before it.
-__device__ __forceinline__ void hash_one(const HashParams& p, int64_t i, int64_t start, int32_t slot,
-                                         int64_t hist_len, int64_t hist_from) {
-  // u[j] = t_{i-j}, newest first.
-  uint32_t u[kMaxN];
+// The newest `n` ids of token i's window, u[j] = t_{i-j}, of a sequence starting at `start`,
+// with the sequence's committed history (slot >= 0: hist_len ids, those before hist_from
+// evicted) before it.
+__device__ __forceinline__ void window_ids(const HashParams& p, int64_t i, int64_t start, int32_t slot,
+                                           int64_t hist_len, int64_t hist_from, int n, uint32_t (&u)[kMaxN]) {
 #pragma unroll
   for (int j = 0; j < kMaxN; ++j) {
-    if (j >= p.N) break;
+    if (j >= n) break;
     const int64_t a = i - j;  // absolute token position if inside this call's sequence
     int64_t t = 0;
     if (a >= start && a >= 0) {
@@ -100,7 +99,62 @@ __device__ __forceinline__ void hash_one(const HashParams& p, int64_t i, int64_t
     }
     u[j] = static_cast<uint32_t>(t);
   }
+}
+
+// Eq. 2 for token i of a sequence starting at `start` (see window_ids).
+__device__ __forceinline__ void hash_one(const HashParams& p, int64_t i, int64_t start, int32_t slot,
+                                         int64_t hist_len, int64_t hist_from) {
+  uint32_t u[kMaxN];
+  window_ids(p, i, start, slot, hist_len, hist_from, p.N, u);
   hash_window(p, i, start, slot, u);
+}
+
+// Eq. 2 for token i and sub-table s alone, bit for bit hash_one's.
+__device__ __forceinline__ uint32_t hash_sub(const HashParams& p, int64_t i, int64_t start, int32_t slot,
+                                             int64_t hist_len, int64_t hist_from, int s) {
+  const int n = s / p.K + 2;
+  uint32_t u[kMaxN];
+  window_ids(p, i, start, slot, hist_len, hist_from, n, u);
+  uint32_t h = 0;
+#pragma unroll
+  for (int j = kMaxN - 1; j >= 0; --j)
+    if (j < n) h = horner_step(h, p.V0, u[j], p.V[s], p.barrett[s]);
+  return h;
+}
+
+// Sticky status for offsets that are not non-decreasing from 0 to T: entry i of num_seqs + 1.
+__device__ __forceinline__ void check_offset(const HashParams& p, int64_t i) {
+  if (i > p.num_seqs) return;
+  const int32_t o = p.offsets[i];
+  const bool bad = (i == 0 && o != 0) || (i == p.num_seqs && o != p.T) ||
+                   (i < p.num_seqs && p.offsets[i + 1] < o);
+  if (bad) set_status(p.status, NGRAM_STATUS_BAD_OFFSETS);
+}
+
+// Where token i stands: its sequence (the largest b with offsets[b] <= i), that sequence's
+// start, and its cache slot (-1 without one) with what the ring holds of it.
+struct TokenPlace {
+  int64_t start, hist_len, hist_from;
+  int32_t slot;
+};
+__device__ __forceinline__ TokenPlace token_place(const HashParams& p, int64_t i, const int32_t* offsets) {
+  int32_t lo = 0, hi = p.num_seqs;
+  while (hi - lo > 1) {
+    const int32_t mid = (lo + hi) >> 1;
+    if (offsets[mid] <= i) lo = mid; else hi = mid;
+  }
+  TokenPlace t{offsets[lo], 0, 0, -1};
+  if (p.ring) {
+    t.slot = p.slots ? p.slots[lo] : lo;
+    if (t.slot < 0 || t.slot >= p.max_seqs) {
+      set_status(p.status, NGRAM_STATUS_BAD_SLOT);
+      t.slot = -1;
+    } else {
+      t.hist_len = p.len[t.slot];
+      t.hist_from = p.valid_from[t.slot];
+    }
+  }
+  return t;
 }
 
 constexpr int kHashSmemOffsets = 4096;  // offsets staged in shared memory when B + 1 fits
@@ -111,13 +165,7 @@ __global__ void __launch_bounds__(256) hash_kernel(const __grid_constant__ HashP
   pdl_launch_dependents();
   pdl_wait();
 
-  // Offsets check (sticky status; the lookups below stay in bounds regardless).
-  if (i <= p.num_seqs) {
-    const int32_t o = p.offsets[i];
-    const bool bad = (i == 0 && o != 0) || (i == p.num_seqs && o != p.T) ||
-                     (i < p.num_seqs && p.offsets[i + 1] < o);
-    if (bad) set_status(p.status, NGRAM_STATUS_BAD_OFFSETS);
-  }
+  check_offset(p, i);  // sticky status; the lookups below stay in bounds regardless
   // Small batches: one coalesced pass brings every offset into shared memory, so the
   // sequence search below costs no dependent global loads.
   const bool staged = p.num_seqs + 1 <= kHashSmemOffsets;
@@ -127,28 +175,8 @@ __global__ void __launch_bounds__(256) hash_kernel(const __grid_constant__ HashP
   }
   if (i >= p.T) return;
 
-  // Sequence of token i: the largest b with offsets[b] <= i.
-  int32_t lo = 0, hi = p.num_seqs;
-  while (hi - lo > 1) {
-    const int32_t mid = (lo + hi) >> 1;
-    if ((staged ? s_off[mid] : p.offsets[mid]) <= i) lo = mid; else hi = mid;
-  }
-  const int64_t start = staged ? s_off[lo] : p.offsets[lo];
-
-  int32_t slot = -1;
-  int64_t hist_len = 0, hist_from = 0;
-  if (p.ring) {
-    slot = p.slots ? p.slots[lo] : lo;
-    if (slot < 0 || slot >= p.max_seqs) {
-      set_status(p.status, NGRAM_STATUS_BAD_SLOT);
-      slot = -1;
-    } else {
-      hist_len = p.len[slot];
-      hist_from = p.valid_from[slot];
-    }
-  }
-
-  hash_one(p, i, start, slot, hist_len, hist_from);
+  const TokenPlace t = token_place(p, i, staged ? s_off : p.offsets);
+  hash_one(p, i, t.start, t.slot, t.hist_len, t.hist_from);
 }
 
 }  // namespace ngram

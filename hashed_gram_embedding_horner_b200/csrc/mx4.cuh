@@ -11,6 +11,7 @@
 #pragma once
 
 #include "common.cuh"
+#include "hash.cuh"
 
 namespace ngram {
 
@@ -233,64 +234,108 @@ struct Mx4Rows {
 
 struct Mx4GatherParams {
   Mx4Rows E[kMaxS];
-  uint32_t Vs[kMaxS];
-  const int32_t* idx;     // [T x S]
-  const int32_t* tokens;  // [T]: only checked (the projection's epilogue reads E_0 by them)
-  uint32_t V0;
-  uint32_t T;
-  int S, row_blocks;      // row_blocks = d / 32, blocks of one sub-row
+  const int32_t* idx;     // [T x S], nullptr: Eq. 2 from h
+  HashParams h;           // tokens, T, V0, S, the moduli V and status in any case
+  int row_blocks;         // d / 32, blocks of one sub-row
   FastDiv by_row, by_sub; // ceil(D / 128) * 4 blocks of a padded row; row_blocks
   int blocks;             // D / 32
   int kt;
+  int tokens;             // a block takes, at most kMx4GatherThreads / S and kMx4GatherMaxTokens
   uint8_t* G;             // [T x D / 2] codes
   uint8_t* Gs;            // scales, in tiles
-  int* status;
 };
 
+constexpr int kMx4GatherThreads = 256;
+constexpr int kMx4GatherMaxTokens = 32;  // of a block
 constexpr int kMx4GatherUnroll = 4;
+constexpr int kMx4GatherOffsets = 1024;  // offsets staged in shared memory when B + 1 fits
 
-// G[i] = the concatenated 4-bit sub-rows of token i, its scales in tiles: one 16-byte code
-// block and one scale byte a thread, kMx4GatherUnroll of each in flight; four neighbouring
-// threads' scale bytes leave as one word. 17/32 bytes an element each way: bound by HBM's
-// random rows at first sight of a row, and by L2 after (G is read back from there).
-__global__ void __launch_bounds__(256) mx4_gather_kernel(const __grid_constant__ Mx4GatherParams p) {
-  const uint32_t total = p.T * p.by_row.d;
-  const uint32_t base = blockIdx.x * (256u * kMx4GatherUnroll) + threadIdx.x;
-  uint4 code[kMx4GatherUnroll];
-  uint32_t scale[kMx4GatherUnroll];
+// The given index of token i in sub-table s, checked; for s = 0 its token too, by which the
+// product's epilogue reads E_0.
+__device__ __forceinline__ uint32_t mx4_given_row(const Mx4GatherParams& p, int64_t i, int s) {
+  const HashParams& h = p.h;
+  const uint32_t row = static_cast<uint32_t>(p.idx[i * h.S + s]);
+  if (row >= h.V[s] || (s == 0 && static_cast<uint32_t>(h.tokens[i]) >= h.V0)) set_status(h.status, NGRAM_STATUS_BAD_TOKEN);
+  return row < h.V[s] ? row : 0;
+}
+
+// Blocks base, base + THREADS, ... (UNROLL of them) of the `total` blocks of the padded rows of
+// tokens i0, i0 + 1, ... whose table rows are s_row[token * S + s]: one 16-byte code block and
+// one scale byte each, all loads in flight together; four neighbouring lanes' scale bytes leave
+// as one word.
+template <int THREADS, int UNROLL>
+__device__ __forceinline__ void mx4_copy_blocks(const Mx4GatherParams& p, int64_t i0, const uint32_t* s_row, uint32_t base,
+                                                uint32_t total) {
+  uint4 code[UNROLL];
+  uint32_t scale[UNROLL];
 #pragma unroll
-  for (int u = 0; u < kMx4GatherUnroll; ++u) {
-    const uint32_t v = base + u * 256u;
+  for (int u = 0; u < UNROLL; ++u) {
+    const uint32_t v = base + u * THREADS;
     scale[u] = 0;
     if (v < total) {
-      const uint32_t i = p.by_row.div(v), b = v - i * p.by_row.d;
-      if (b == 0 && p.tokens && static_cast<uint32_t>(p.tokens[i]) >= p.V0) set_status(p.status, NGRAM_STATUS_BAD_TOKEN);
+      const uint32_t k = p.by_row.div(v), b = v - k * p.by_row.d;
       if (b < static_cast<uint32_t>(p.blocks)) {
         const uint32_t s = p.by_sub.div(b), c = b - s * p.row_blocks;
-        uint32_t row = static_cast<uint32_t>(p.idx[static_cast<int64_t>(i) * p.S + s]);
-        if (row >= p.Vs[s]) {
-          set_status(p.status, NGRAM_STATUS_BAD_TOKEN);
-          row = 0;
-        }
-        const size_t at = static_cast<size_t>(row) * p.row_blocks + c;
+        const size_t at = static_cast<size_t>(s_row[k * p.h.S + s]) * p.row_blocks + c;
         code[u] = ld_stream_v4(p.E[s].codes + at * 16);
         scale[u] = __ldg(p.E[s].scales + at);
       }
     }
   }
 #pragma unroll
-  for (int u = 0; u < kMx4GatherUnroll; ++u) {
-    const uint32_t v = base + u * 256u;
+  for (int u = 0; u < UNROLL; ++u) {
+    const uint32_t v = base + u * THREADS;
+    if (v >= total) continue;  // a padded row is a multiple of 4 blocks: four neighbours alike
+    const uint32_t quad = 0xFu << (threadIdx.x & 28);
     uint32_t w = scale[u] << ((threadIdx.x & 3) * 8);
-    w |= __shfl_xor_sync(0xffffffffu, w, 1);
-    w |= __shfl_xor_sync(0xffffffffu, w, 2);
-    if (v >= total) continue;
-    const uint32_t i = p.by_row.div(v), b = v - i * p.by_row.d;
+    w |= __shfl_xor_sync(quad, w, 1);
+    w |= __shfl_xor_sync(quad, w, 2);
+    const uint32_t k = p.by_row.div(v), b = v - k * p.by_row.d;
     if (b < static_cast<uint32_t>(p.blocks))
-      *reinterpret_cast<uint4*>(p.G + (static_cast<size_t>(i) * p.blocks + b) * 16) = code[u];
+      *reinterpret_cast<uint4*>(p.G + (static_cast<size_t>(i0 + k) * p.blocks + b) * 16) = code[u];
     if ((threadIdx.x & 3) == 0)
-      *reinterpret_cast<uint32_t*>(p.Gs + mx4_tile_at(i, static_cast<int>(b), p.kt)) = w;
+      *reinterpret_cast<uint32_t*>(p.Gs + mx4_tile_at(i0 + k, static_cast<int>(b), p.kt)) = w;
   }
+}
+
+// G[i] = the concatenated 4-bit sub-rows of token i, its scales in tiles. A block takes a few
+// tokens: their places in their sequences, a thread each; their row indices (Eq. 2, or idx), a
+// thread each; then their rows. Hashing in the launch that gathers takes 8.6 us at a decode step
+// of 1280 tokens, D = 4096, where two launches took 6.7 and 5.6. 17/32 bytes an element each way,
+// random rows from HBM: 71 us at 65536 tokens of D = 4096, which move 302 MB with the sectors of
+// the scales read whole.
+//
+// Running it beside the product (as resident blocks that the product waits for 256 rows at a
+// time, or in the product's idle warps) was slower, 522 and 765 us for the two against 503 one
+// after the other: the product keeps the L2 busy, and the gather's loads queue behind its.
+__global__ void __launch_bounds__(kMx4GatherThreads) mx4_gather_kernel(const __grid_constant__ Mx4GatherParams p) {
+  __shared__ int32_t s_off[kMx4GatherOffsets];
+  __shared__ TokenPlace s_place[kMx4GatherMaxTokens];
+  __shared__ uint32_t s_row[kMx4GatherThreads];
+  const HashParams& h = p.h;
+  const int64_t i0 = static_cast<int64_t>(blockIdx.x) * p.tokens;
+  const int n = h.T - i0 < p.tokens ? static_cast<int>(h.T - i0) : p.tokens;
+  if (!p.idx) {
+    for (int64_t k = static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x; k <= h.num_seqs;
+         k += static_cast<int64_t>(gridDim.x) * blockDim.x)
+      check_offset(h, k);
+    const bool staged = h.num_seqs + 1 <= kMx4GatherOffsets;
+    if (staged)
+      for (int k = threadIdx.x; k <= h.num_seqs; k += blockDim.x) s_off[k] = h.offsets[k];
+    __syncthreads();
+    if (static_cast<int>(threadIdx.x) < n) s_place[threadIdx.x] = token_place(h, i0 + threadIdx.x, staged ? s_off : h.offsets);
+    __syncthreads();
+  }
+  if (static_cast<int>(threadIdx.x) < n * h.S) {
+    const int k = threadIdx.x / h.S, s = threadIdx.x - k * h.S;
+    const TokenPlace t = s_place[k];
+    s_row[threadIdx.x] = p.idx ? mx4_given_row(p, i0 + k, s)
+                               : hash_sub(h, i0 + k, t.start, t.slot, t.hist_len, t.hist_from, s);
+  }
+  __syncthreads();
+  const uint32_t total = static_cast<uint32_t>(n) * p.by_row.d;
+  for (uint32_t base = threadIdx.x; base < total; base += kMx4GatherThreads * kMx4GatherUnroll)
+    mx4_copy_blocks<kMx4GatherThreads, kMx4GatherUnroll>(p, i0, s_row, base, total);
 }
 
 // ------------------------------------------------------------------ product

@@ -4,18 +4,25 @@
 
 namespace {
 
-// A kernel's shared memory beyond 48 KB, asked for once a device (a bit of `done` each).
-template <typename K>
-int opt_in_smem(K kern, int bytes, std::atomic<uint64_t>& done, bool wide_clusters = false) {
+// Runs `set` (a kernel's attributes) once a device, a bit of `done` each.
+template <typename F>
+int once_a_device(std::atomic<uint64_t>& done, F set) {
   int dev = -1;
   if (cudaGetDevice(&dev) != cudaSuccess) return NGRAM_ERR_CUDA;
   const uint64_t bit = uint64_t(1) << (dev & 63);
   if (dev < 64 && (done.load(std::memory_order_acquire) & bit)) return NGRAM_OK;
-  if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes) != cudaSuccess ||
-      (wide_clusters && cudaFuncSetAttribute(kern, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) != cudaSuccess))
-    return NGRAM_ERR_CUDA;
+  if (!set()) return NGRAM_ERR_CUDA;
   if (dev < 64) done.fetch_or(bit, std::memory_order_release);
   return NGRAM_OK;
+}
+
+// A kernel's shared memory beyond 48 KB.
+template <typename K>
+int opt_in_smem(K kern, int bytes, std::atomic<uint64_t>& done, bool wide_clusters = false) {
+  return once_a_device(done, [&] {
+    return cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes) == cudaSuccess &&
+           (!wide_clusters || cudaFuncSetAttribute(kern, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) == cudaSuccess);
+  });
 }
 
 // Makes the device that owns `p` current for a call, and the caller's again after it. Calls
@@ -146,35 +153,39 @@ int launch_mx4_tiles(Mx4GemmParams prm, const Mx4Operands& o, int sms, cudaStrea
 // ones are too few. Measured on B200, bf16 out (us, wide / 128 / 64): 32768 x 4096 x 4096 206 /
 // 310 / 548, 1280 x 4096 x 4096 17.3 / 20.2 / 28.2, 512 x 4096 x 4096 11.3 / 9.6 / 13.5,
 // 333 x 1111 x 2080 11.6 / 8.7 / 6.6, 128 x 512 x 512 6.8 / 4.7 / 4.0.
-template <typename OutT>
-int launch_mx4_gemm(const Mx4GemmParams& prm, const Mx4Operands& o, int sms, cudaStream_t st) {
-  if (sms < 2) return NGRAM_ERR_CUDA;
-  const double kb = (prm.K + 255) / 256;
+int mx4_tile_width(int M, int N, int K, int sms) {
+  const double kb = (K + 255) / 256;
   auto cost = [&](int rows, int cols, int workers, double us_kb, double us_tile) {
-    const int64_t tiles = static_cast<int64_t>((prm.M + rows - 1) / rows) * ((prm.N + cols - 1) / cols);
+    const int64_t tiles = (static_cast<int64_t>(M) + rows - 1) / rows * ((static_cast<int64_t>(N) + cols - 1) / cols);
     return static_cast<double>((tiles + workers - 1) / workers) * (kb * us_kb + us_tile);
   };
   const double wide = cost(256, 256, sms / 2, 0.42, 1.6), mid = cost(128, 128, sms, 0.33, 1.0),
                narrow = cost(128, 64, sms, 0.29, 0.5);
-  if (wide <= mid && wide <= narrow) return launch_mx4_tiles<256, 6, OutT, true>(prm, o, sms, st);
-  if (mid <= narrow) return launch_mx4_tiles<128, 6, OutT, false>(prm, o, sms, st);
-  return launch_mx4_tiles<64, 8, OutT, false>(prm, o, sms, st);
+  return wide <= mid && wide <= narrow ? 256 : (mid <= narrow ? 128 : 64);
 }
 
-// Workspace of the layer on 4-bit tables: [head | T x S indices | T x D / 2 codes | scale tiles]
+template <typename OutT>
+int launch_mx4_gemm(const Mx4GemmParams& prm, const Mx4Operands& o, int sms, cudaStream_t st) {
+  if (sms < 2) return NGRAM_ERR_CUDA;
+  switch (mx4_tile_width(prm.M, prm.N, prm.K, sms)) {
+    case 256: return launch_mx4_tiles<256, 6, OutT, true>(prm, o, sms, st);
+    case 128: return launch_mx4_tiles<128, 6, OutT, false>(prm, o, sms, st);
+    default: return launch_mx4_tiles<64, 8, OutT, false>(prm, o, sms, st);
+  }
+}
+
+// Workspace of the layer on 4-bit tables: [head | T x D / 2 codes | scale tiles]
 struct Mx4LayerWs {
-  int32_t* idx;
   uint8_t *G, *Gs;
   size_t bytes;
 };
 Mx4LayerWs mx4_layer_ws(const ngram_embed_plan* p, int64_t T, void* ws) {
   Mx4LayerWs w{};
-  const size_t at_g = ws_base(p, T);
+  const size_t at_g = kHeadBytes;
   const size_t at_s = at_g + round256(static_cast<size_t>(T) * static_cast<size_t>(p->D) / 2);
   w.bytes = at_s + round256(mx4_tiled_scale_bytes(T, p->D));
   if (ws) {
     auto* b = static_cast<uint8_t*>(ws);
-    w.idx = idx_ptr(ws);
     w.G = b + at_g;
     w.Gs = b + at_s;
   }
@@ -194,19 +205,19 @@ int check_mx4_layer(const ngram_embed_plan* p, const int32_t* tokens, const void
   return NGRAM_OK;
 }
 
-int project_mx4(const ngram_embed_plan* p, const int32_t* tokens, const int32_t* idx, int64_t T, const void* E0,
-                const ngram_mx4* E_nk, const ngram_mx4* W, void* out, const Mx4LayerWs& w, void* ws, cudaStream_t st) {
+// The gather of the call's sub-rows (indices from idx, or hashed from h's sequences), then the
+// product with E_0 added.
+int project_mx4(const ngram_embed_plan* p, const HashParams& h, const int32_t* idx, const void* E0,
+                const ngram_mx4* E_nk, const ngram_mx4* W, void* out, const Mx4LayerWs& w, cudaStream_t st) {
+  if (p->sms < 2) return NGRAM_ERR_CUDA;
+  const int64_t T = h.T;
   Mx4GatherParams g{};
   for (int s = 0; s < p->S; ++s) {
     g.E[s].codes = static_cast<const uint8_t*>(E_nk[s].codes);
     g.E[s].scales = static_cast<const uint8_t*>(E_nk[s].scales);
-    g.Vs[s] = static_cast<uint32_t>(p->V[s]);
   }
   g.idx = idx;
-  g.tokens = tokens;
-  g.V0 = static_cast<uint32_t>(p->V0);
-  g.T = static_cast<uint32_t>(T);
-  g.S = p->S;
+  g.h = h;
   g.row_blocks = p->d / kMxBlock;
   g.kt = (p->D + 127) / 128;
   g.by_row.set(static_cast<uint32_t>(g.kt) * 4);
@@ -214,28 +225,31 @@ int project_mx4(const ngram_embed_plan* p, const int32_t* tokens, const int32_t*
   g.blocks = p->D / kMxBlock;
   g.G = w.G;
   g.Gs = w.Gs;
-  g.status = status_ptr(ws);
-  const int64_t vecs = T * g.kt * 4;
-  constexpr int64_t per_block = 256 * kMx4GatherUnroll;
-  if (vecs + per_block > UINT32_MAX) return NGRAM_ERR_UNSUPPORTED;  // numbered in 32 bits
-  int rc = launch(mx4_gather_kernel, dim3(static_cast<unsigned>((vecs + per_block - 1) / per_block)), dim3(256), 0, st,
-                  p->pdl, 1, g);
+  // tokens a block: kMx4GatherUnroll vectors a thread where the call has blocks to spare
+  static_assert(8 * kMaxS <= kMx4GatherThreads, "a block hashes its tokens' indices in one pass");
+  int tokens = T < 32 * static_cast<int64_t>(p->sms) ? 8 : kMx4GatherThreads * kMx4GatherUnroll / static_cast<int>(g.by_row.d);
+  if (tokens > kMx4GatherThreads / p->S) tokens = kMx4GatherThreads / p->S;
+  if (tokens > kMx4GatherMaxTokens) tokens = kMx4GatherMaxTokens;
+  g.tokens = tokens < 8 ? 8 : tokens;
+  int rc = launch(mx4_gather_kernel, dim3(static_cast<unsigned>((T + g.tokens - 1) / g.tokens)), dim3(kMx4GatherThreads), 0,
+                  st, p->pdl, 1, g);
   if (rc) return rc;
   Mx4GemmParams prm{};
   prm.M = static_cast<int>(T);
   prm.N = p->D;
   prm.K = p->D;
   prm.scale = p->out_scale / static_cast<float>(p->S + 1);
-  prm.tokens = tokens;
+  prm.tokens = h.tokens;
   prm.E0 = E0;
   prm.V0 = static_cast<uint32_t>(p->V0);
   prm.out = out;
   prm.ldo = p->D;
   prm.vec16 = 1;  // rows of a multiple of 32 elements, out and E_0 16-byte aligned
   prm.vec32 = aligned32(out) && aligned32(E0) ? 1 : 0;
-  prm.status = status_ptr(ws);
+  prm.status = h.status;
   const Mx4Operands o{w.G, w.Gs, static_cast<const uint8_t*>(W->codes), static_cast<const uint8_t*>(W->scales)};
-  return p->dtype == NGRAM_F32 ? launch_mx4_gemm<float>(prm, o, p->sms, st) : launch_mx4_gemm<uint16_t>(prm, o, p->sms, st);
+  return p->dtype == NGRAM_F32 ? launch_mx4_gemm<float>(prm, o, p->sms, st)
+                               : launch_mx4_gemm<uint16_t>(prm, o, p->sms, st);
 }
 
 // ---- lookup and gradient of one table ----
@@ -550,7 +564,8 @@ int ngram_embed_project_mx4(const ngram_embed_plan* plan, const int32_t* tokens,
   if (rc) return rc;
   const DeviceScope dev(plan);
   if (dev.rc) return dev.rc;
-  return project_mx4(plan, tokens, idx, num_tokens, E0, E_nk, W, out, w, workspace, static_cast<cudaStream_t>(stream));
+  return project_mx4(plan, hash_params(plan, tokens, nullptr, 0, num_tokens, nullptr, nullptr, workspace), idx, E0, E_nk, W,
+                     out, w, static_cast<cudaStream_t>(stream));
 }
 
 int ngram_embed_fwd_mx4(const ngram_embed_plan* plan, const int32_t* tokens, const int32_t* seq_offsets,
@@ -569,10 +584,8 @@ int ngram_embed_fwd_mx4(const ngram_embed_plan* plan, const int32_t* tokens, con
   if (cache && (rc = validate_cache(plan, cache))) return rc;
   const DeviceScope dev(plan);
   if (dev.rc) return dev.rc;
-  const cudaStream_t st = static_cast<cudaStream_t>(stream);
-  if ((rc = launch_hash(plan, tokens, seq_offsets, num_seqs, num_tokens, cache, cache_slots, w.idx, workspace, st)))
-    return rc;
-  return project_mx4(plan, tokens, w.idx, num_tokens, E0, E_nk, W, out, w, workspace, st);
+  return project_mx4(plan, hash_params(plan, tokens, seq_offsets, num_seqs, num_tokens, cache, cache_slots, workspace),
+                     nullptr, E0, E_nk, W, out, w, static_cast<cudaStream_t>(stream));
 }
 
 size_t ngram_embedding_workspace_bytes(int64_t max_ids, int64_t D) {

@@ -684,9 +684,8 @@ int set_device(const ngram_embed_plan* p) {
   return NGRAM_OK;
 }
 
-int launch_hash(const ngram_embed_plan* p, const int32_t* tokens, const int32_t* offsets, int32_t num_seqs,
-                int64_t T, const ngram_cache* cache, const int32_t* slots, int32_t* idx_out, void* ws,
-                cudaStream_t st, int32_t* win_out = nullptr, int32_t* entry_out = nullptr, int32_t positions = 0) {
+HashParams hash_params(const ngram_embed_plan* p, const int32_t* tokens, const int32_t* offsets, int32_t num_seqs,
+                       int64_t T, const ngram_cache* cache, const int32_t* slots, void* ws) {
   HashParams h{};
   h.tokens = tokens;
   h.offsets = offsets;
@@ -708,11 +707,18 @@ int launch_hash(const ngram_embed_plan* p, const int32_t* tokens, const int32_t*
     h.max_seqs = cache->max_seqs;
     h.slots = slots;
   }
+  h.status = status_ptr(ws);
+  return h;
+}
+
+int launch_hash(const ngram_embed_plan* p, const int32_t* tokens, const int32_t* offsets, int32_t num_seqs,
+                int64_t T, const ngram_cache* cache, const int32_t* slots, int32_t* idx_out, void* ws,
+                cudaStream_t st, int32_t* win_out = nullptr, int32_t* entry_out = nullptr, int32_t positions = 0) {
+  HashParams h = hash_params(p, tokens, offsets, num_seqs, T, cache, slots, ws);
   h.idx_out = idx_out;
   h.win_out = win_out;
   h.entry_out = entry_out;
   h.positions = positions;
-  h.status = status_ptr(ws);
   const int64_t work = T > num_seqs + 1 ? T : num_seqs + 1;
   const int64_t blocks = (work + 255) / 256;
   return launch(hash_kernel, dim3(static_cast<unsigned>(blocks)), dim3(256), 0, st, p->pdl, 1, h);

@@ -374,7 +374,7 @@ int ngram_mx4_product(const ngram_mx4* A, const ngram_mx4* B, int64_t M, int64_t
  * and the status bits are those of ngram_embed_fwd. The result is Eq. 3 on the values that the
  * 4-bit tables stand for (fp32 sums, one rounding). Needs N >= 2 and d a multiple of 32 (else
  * NGRAM_ERR_UNSUPPORTED; any plan dtype).
- *   workspace  >= ngram_embed_mx4_workspace_bytes(plan, num_tokens): head, indices, the
+ *   workspace  >= ngram_embed_mx4_workspace_bytes(plan, num_tokens): head, then the
  *              gathered sub-rows (17/32 bytes an element); 0 for a plan it does not serve */
 size_t ngram_embed_mx4_workspace_bytes(const ngram_embed_plan* plan, int64_t max_tokens);
 int ngram_embed_fwd_mx4(const ngram_embed_plan* plan, const int32_t* tokens,

@@ -185,6 +185,42 @@ def test_layer_from_4bit_tables(ne, case, lengths):
     assert (np.abs(f64(out) - want) <= acc + HALF[dtype] * (np.abs(want) + acc)).all()
 
 
+@pytest.mark.parametrize("dtype,D,N,K,lengths", [
+    (BF16, 1024, 3, 1, [3000, 0, 1, 700, 299]), (F32, 1024, 3, 1, [3999]), (BF16, 1056, 4, 1, [2049, 2048]),
+    (BF16, 1280, 5, 2, [1] * 3000),
+])
+def test_layer_of_many_tokens(ne, dtype, D, N, K, lengths):
+    """Enough rows for the widest tiles, whose kernel gathers its rows itself; twice on one
+    workspace (its counters come back to zero), and once with ids out of range."""
+    S = (N - 1) * K
+    V0, V = 5000, [3001 + 10 * s for s in range(S)]
+    L = make_layer(ne, D, V0, D, N, K, V, dtype)
+    off = gen.offsets_from_lengths(lengths)
+    T = int(off[-1])
+    rng = np.random.default_rng(T)
+    ws = ne.new_embed_mx4_workspace(L["plan"], T)
+    off_d = torch.from_numpy(off).cuda()
+    for bad in (False, False, True):
+        tokens = rng.integers(0, V0, T).astype(np.int32)
+        good = tokens.copy()
+        if bad:
+            tokens[::501], good[::501] = np.where(np.arange(len(tokens[::501])) % 2, V0, -3), 0
+        out = torch.full((T, D), 3.0, dtype=dtype, device="cuda")
+        ne.ngram_embed_fwd_mx4(L["plan"], torch.from_numpy(tokens).cuda(), off_d, L["E0"], L["E"], L["W"], out, ws)
+        assert ne.ngram_embed_get_status(ws) == (0x1 if bad else 0)
+        want, acc, idx = ref.layer(V0, N, K, V, good, off, f64(L["E0"]), L["E_vals"], L["W_vals"])
+        assert (np.abs(f64(out) - want) <= acc + HALF[dtype] * (np.abs(want) + acc)).all()
+    assert not bool(ws[256:33024].any())
+    ne.ngram_embed_clear_status(ws)
+    again = torch.empty_like(out)
+    ne.ngram_embed_project_mx4(L["plan"], torch.from_numpy(good).cuda(), torch.from_numpy(idx.astype(np.int32)).cuda(),
+                               L["E0"], L["E"], L["W"], again, ws)
+    assert torch.equal(again, out) and ne.ngram_embed_get_status(ws) == 0
+    off_d[-1] -= 1  # tokens past the last sequence's end
+    ne.ngram_embed_fwd_mx4(L["plan"], torch.from_numpy(good).cuda(), off_d, L["E0"], L["E"], L["W"], again, ws)
+    assert ne.ngram_embed_get_status(ws) == 0x2
+
+
 def test_layer_through_the_ring(ne):
     """Decode: windows continue into each slot's committed history, also through other slots."""
     V0, D, N, K, V, dtype = LAYERS[2]

@@ -78,8 +78,8 @@ def test_layer_refusals(ne):
     plan = _plan(ne)
     tabs = (ne._Mx4 * 4)(*[ne._Mx4(0x30000, 0x40000)] * 4)
     need = lib.ngram_embed_mx4_workspace_bytes(plan.handle, 100)
-    # head, indices, codes of 100 rows of 128, one row block of one scale tile
-    assert need == 33024 + (100 * 16 + 255) // 256 * 256 + 100 * 64 + 0 + 512
+    # head, codes of 100 rows of 128, one row block of one scale tile
+    assert need == 33024 + 100 * 64 + 512
     assert lib.ngram_embed_mx4_workspace_bytes(plan.handle, -1) == 0
     assert lib.ngram_embed_mx4_workspace_bytes(None, 10) == 0
     W = ctypes.byref(ne._Mx4(0x50000, 0x60000))
