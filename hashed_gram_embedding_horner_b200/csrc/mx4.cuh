@@ -566,7 +566,8 @@ __device__ __forceinline__ void mx4_store_rows(const Mx4GemmParams& p, int row0,
 // One tile's epilogue for one of the eight warps: TMEM lanes q * 32 .. + 31 (a row a lane), the
 // tile's column half g, 32 columns at a time: accumulators from TMEM, the row's E_0 added,
 // scaled, rounded and stored by the lane that holds them, 32 bytes (a whole sector) an access.
-// Nothing passes through shared memory, which the loads and the MMAs' operands keep busy. E_0
+// (Through shared memory, with whole rows in by cp.async and out by TMA stores, a tile takes as
+// long: the epilogue then waits for the accumulator a third of the time.) E_0
 // rows are random reads: the columns of all four chunks (bf16; two of them f32) are asked for
 // before the accumulator is ready, and the next tile's rows are brought toward L2.
 // `ready` waits for the accumulator (false: abort); `release` hands it back.
@@ -767,8 +768,8 @@ __global__ void __launch_bounds__(kMxThreads, 1)
     }
   } else if (warp == 1) {
     // ------------------------------------------------------------ scales to TMEM, MMA (CTA 0)
-    // The whole warp runs the loop, so that its addresses and descriptors are warp-uniform
-    // values, and one elected lane issues.
+    // One elected lane. (Chosen by `lane == 0`, whose values the compiler does not take for
+    // warp-uniform, the loop needed about 1000 cycles a k-block to issue, whatever its MMAs took.)
     if (rank == 0 && elect_one()) {
       int stage = 0;
       uint32_t phase = 0;

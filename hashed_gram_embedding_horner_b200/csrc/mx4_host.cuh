@@ -168,7 +168,7 @@ template <typename OutT>
 int launch_mx4_gemm(const Mx4GemmParams& prm, const Mx4Operands& o, int sms, cudaStream_t st) {
   if (sms < 2) return NGRAM_ERR_CUDA;
   switch (mx4_tile_width(prm.M, prm.N, prm.K, sms)) {
-    case 256: return launch_mx4_tiles<256, 6, OutT, true>(prm, o, sms, st);
+    case 256: return launch_mx4_tiles<256, 5, OutT, true>(prm, o, sms, st);
     case 128: return launch_mx4_tiles<128, 6, OutT, false>(prm, o, sms, st);
     default: return launch_mx4_tiles<64, 8, OutT, false>(prm, o, sms, st);
   }
