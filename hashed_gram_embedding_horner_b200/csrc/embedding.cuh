@@ -77,6 +77,7 @@ __device__ __forceinline__ void store8(OutT* dst, const float (&x)[8]) {
 
 template <int TABLE, typename OutT, int U>
 __global__ void __launch_bounds__(256) lookup_kernel(const __grid_constant__ LookupParams p) {
+  pdl_wait();
   const RowPart<U> part(p.map);
   if (!part.live) return;
   constexpr int R = RowPart<U>::R;
@@ -421,6 +422,8 @@ constexpr int kGradLoads = 8;
 template <typename T, int PIECE>
 __global__ void __launch_bounds__(256) grad_reduce_kernel(const __grid_constant__ GradParams p) {
   constexpr int kLanes = PIECE < 32 ? PIECE : 32;  // sorted positions a lane holds one of at a time
+  pdl_launch_dependents();
+  pdl_wait();
   const uint64_t item = static_cast<uint64_t>(blockIdx.x) * 8 + (threadIdx.x >> 5);
   const int lane = threadIdx.x & 31;
   const uint32_t piece = static_cast<uint32_t>(item / p.chunks);
@@ -487,6 +490,7 @@ __global__ void __launch_bounds__(256) grad_reduce_kernel(const __grid_constant_
 constexpr int kJoinLoads = 8;
 
 __global__ void __launch_bounds__(256, 4) grad_join_kernel(const __grid_constant__ GradParams p) {
+  pdl_wait();
   const int chunks = (p.D + 127) / 128;
   const uint64_t item = static_cast<uint64_t>(blockIdx.x) * 8 + (threadIdx.x >> 5);
   const int lane = threadIdx.x & 31;
@@ -624,6 +628,7 @@ __global__ void __launch_bounds__(kClusterThreads, 1) sort_cluster_kernel(const 
   constexpr int kWarpItems = 32 * ITEMS;
   extern __shared__ __align__(16) uint8_t cluster_raw[];
   auto& m = *reinterpret_cast<ClusterSmem<ITEMS>*>(cluster_raw);
+  pdl_launch_dependents();
   const SortParams& p = a.s;
   const int tid = threadIdx.x, lane = tid & 31, w = tid >> 5;
   const uint32_t rank = cluster_ctarank(), ctas = gridDim.x;

@@ -160,6 +160,8 @@ __device__ __forceinline__ float mx4_inverse(int e) { return __uint_as_float(sta
 // element, bound by HBM.
 template <typename T, bool VEC, int U>
 __global__ void __launch_bounds__(256) mx4_quantize_kernel(const __grid_constant__ Mx4QuantParams p) {
+  pdl_launch_dependents();
+  pdl_wait();
   const RowPart<U> part(p.map);
   if (!part.live) return;
   constexpr int R = RowPart<U>::R;
@@ -312,6 +314,8 @@ __global__ void __launch_bounds__(kMx4GatherThreads) mx4_gather_kernel(const __g
   __shared__ int32_t s_off[kMx4GatherOffsets];
   __shared__ TokenPlace s_place[kMx4GatherMaxTokens];
   __shared__ uint32_t s_row[kMx4GatherThreads];
+  pdl_launch_dependents();
+  pdl_wait();
   const HashParams& h = p.h;
   const int64_t i0 = static_cast<int64_t>(blockIdx.x) * p.tokens;
   const int n = h.T - i0 < p.tokens ? static_cast<int>(h.T - i0) : p.tokens;
@@ -569,12 +573,11 @@ __device__ __forceinline__ void mx4_store_rows(const Mx4GemmParams& p, int row0,
 // (Through shared memory, with whole rows in by cp.async and out by TMA stores, a tile takes as
 // long: the epilogue then waits for the accumulator a third of the time.) E_0
 // rows are random reads: the columns of all four chunks (bf16; two of them f32) are asked for
-// before the accumulator is ready, and the next tile's rows are brought toward L2.
+// before the accumulator is ready.
 // `ready` waits for the accumulator (false: abort); `release` hands it back.
 template <typename L, int BN, typename OutT, typename Ready, typename Release>
 __device__ __forceinline__ bool mx4_epilogue(const Mx4GemmParams& p, uint32_t* stg, uint32_t tmem_base, int q, int g, int lane,
-                                             int row0, int col0, int next_row0, int next_col0, int acc, Ready ready,
-                                             Release release) {
+                                             int row0, int col0, int acc, Ready ready, Release release) {
   constexpr int kChunks = BN / 64;
   // The columns shared with the other accumulator go first: the last chunk of accumulator 0
   // (of the half g = 1) or the first of accumulator 1 (g = 0). The other half has nothing to
@@ -592,12 +595,6 @@ __device__ __forceinline__ bool mx4_epilogue(const Mx4GemmParams& p, uint32_t* s
   auto load_e = [&](int slot, int col) { e[slot].load(e0 && col < p.N ? e0 + col : nullptr, p.vec32 != 0); };
 #pragma unroll
   for (int cc = 0; cc < kDepth; ++cc) load_e(cc, col0 + chunk_col(cc));
-  if (const OutT* next = mx4_e0_row<OutT>(p, next_row0 + lane)) {  // the next tile's E_0, a row a lane
-    const int c0 = next_col0 + g * (BN / 2);
-#pragma unroll
-    for (int b = 0; b < BN / 2; b += 128 / static_cast<int>(sizeof(OutT)))
-      if (c0 + b < p.N) prefetch_l2(next + c0 + b);
-  }
   if (!ready()) return false;
   if (L::kOverlap && !shares) release();
   const uint32_t taddr = tmem_base + (static_cast<uint32_t>(q * 32) << 16) + static_cast<uint32_t>(acc * L::kAccStride);
@@ -718,6 +715,7 @@ __global__ void __launch_bounds__(kMxThreads, 1)
   if (PAIR) cluster_sync();
   tc_fence_after();
   const uint32_t tmem_base = *tmem_slot;
+  pdl_wait();  // nothing above touches global memory
 
   const int num_tiles = p.num_m_blocks * p.num_n_blocks;
   const int KB = p.num_k_blocks;
@@ -726,7 +724,9 @@ __global__ void __launch_bounds__(kMxThreads, 1)
   if (warp == 0) {
     // ------------------------------------------------------------ TMA producer
     if (lane == 0) {
-      const uint64_t pol = l2_policy_evict_normal();
+      // B (a weight that every row block reads) stays in L2 before the rest: 95.7 -> 91.9 us for the
+      // layer at D = 2048, 32768 tokens
+      const uint64_t pol = l2_policy_evict_normal(), pol_b = l2_policy_evict_last();
       int stage = 0;
       uint32_t phase = 0;
       bool ok = true;
@@ -748,15 +748,15 @@ __global__ void __launch_bounds__(kMxThreads, 1)
           if (PAIR) {
             const uint32_t bar = map_to_cta(full_bar(stage), 0);
             if (a_rows) tma_load_2d_pair(at, map_a, kb * 128, m_blk * 128, bar, pol);
-            if (b_rows) tma_load_2d_pair(at + L::kABytes, map_b, kb * 128, brow, bar, pol);
+            if (b_rows) tma_load_2d_pair(at + L::kABytes, map_b, kb * 128, brow, bar, pol_b);
             tma_load_2d_pair(at + L::kSfaOffset, &maps.SA, kb * 256, m_blk, bar, pol);
-            tma_load_2d_pair(at + L::kSfbOffset, &maps.SB, kb * 256, n_blk * BN >> 7, bar, pol);
+            tma_load_2d_pair(at + L::kSfbOffset, &maps.SB, kb * 256, n_blk * BN >> 7, bar, pol_b);
           } else {
             const uint32_t bar = full_bar(stage);
             tma_load_2d(at, map_a, kb * 128, m_blk * 128, bar, pol);
-            tma_load_2d(at + L::kABytes, map_b, kb * 128, brow, bar, pol);
+            tma_load_2d(at + L::kABytes, map_b, kb * 128, brow, bar, pol_b);
             tma_load_2d(at + L::kSfaOffset, &maps.SA, kb * 256, m_blk, bar, pol);
-            tma_load_2d(at + L::kSfbOffset, &maps.SB, kb * 256, n_blk * BN >> 7, bar, pol);
+            tma_load_2d(at + L::kSfbOffset, &maps.SB, kb * 256, n_blk * BN >> 7, bar, pol_b);
           }
           if (++stage == STAGES) { stage = 0; phase ^= 1u; }
         }
@@ -831,10 +831,7 @@ __global__ void __launch_bounds__(kMxThreads, 1)
           if (lane == 0) mbar_arrive_remote_relaxed(map_to_cta(bar, 0));
         }
       };
-      const int next = tile + workers;
-      const int next_row0 = next < num_tiles ? ((next / p.num_n_blocks) * kRanks + static_cast<int>(rank)) * 128 + q * 32 : p.M;
-      if (!mx4_epilogue<L, BN, OutT>(p, stg, tmem_base, q, g, lane, m_blk * 128 + q * 32, n_blk * BN, next_row0,
-                                     (next % p.num_n_blocks) * BN, acc, ready, release))
+      if (!mx4_epilogue<L, BN, OutT>(p, stg, tmem_base, q, g, lane, m_blk * 128 + q * 32, n_blk * BN, acc, ready, release))
         break;
     }
   }
