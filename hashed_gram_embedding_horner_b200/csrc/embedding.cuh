@@ -329,6 +329,9 @@ struct GradParams {
   int D, chunks;          // chunks = ceil(D / 256)
   float scale;
   float* partial;         // [pieces x 2 x D]: 0 the run a piece begins in, 1 the one it ends in
+  int32_t* crossing;      // [2]: runs that cross pieces: of few pieces, of more than kJoinShort more
+  int32_t* lists;         // [2 x pieces]: the pieces that they begin in, in no order
+  uint32_t pieces;
   float* out;             // compact: [unique x D]; dense: [V x D], added to
   int dense;
 };
@@ -373,6 +376,7 @@ __global__ void __launch_bounds__(kSortThreads) grad_number_kernel(const __grid_
     }
     if (i < p.n && i % p.piece == 0) p.piece_run[i / p.piece] = static_cast<int32_t>(run) - 1;
   }
+  if (blockIdx.x == 0 && threadIdx.x < 2) p.crossing[threadIdx.x] = 0;
   if (p.count_out && blockIdx.x + 1 == p.tiles && threadIdx.x == 0) *p.count_out = static_cast<int32_t>(base + total);
 }
 
@@ -415,6 +419,8 @@ __device__ __forceinline__ void grad_finish(const GradParams& p, int32_t run, ui
 __device__ __forceinline__ float4* grad_partial(const GradParams& p, uint32_t piece, int which, int c) {
   return reinterpret_cast<float4*>(p.partial + (static_cast<size_t>(piece) * 2 + which) * p.D + c);
 }
+
+constexpr int kJoinShort = 16;  // pieces after its first that a warp alone joins a run of
 
 // One warp a (piece, 256 columns), eight columns a lane, kGradLoads rows in flight.
 constexpr int kGradLoads = 8;
@@ -478,65 +484,106 @@ __global__ void __launch_bounds__(256) grad_reduce_kernel(const __grid_constant_
     }
   }
   const uint64_t end = static_cast<uint64_t>(begin) + PIECE;
-  if (end < p.n && p.key[end] == cur) leave(open ? 0 : 1);  // it goes on in the next piece
-  else if (open) leave(0);
-  else finish(cur);
+  if (end < p.n && p.key[end] == cur) {  // it goes on in the next piece
+    leave(open ? 0 : 1);
+    if (!open && c == 0) {  // it begins here: for the join (one lane of the piece's warps)
+      const uint64_t far = end + static_cast<uint64_t>(kJoinShort) * PIECE;
+      const int which = far < p.n && p.key[far] == cur ? 1 : 0;
+      p.lists[static_cast<size_t>(which) * p.pieces + atomicAdd(p.crossing + which, 1)] = static_cast<int32_t>(piece);
+    }
+  } else if (open) {
+    leave(0);
+  } else {
+    finish(cur);
+  }
 }
 
-// The runs that cross pieces: one warp a (piece whose last run begins in it and goes on, 128
-// columns) adds the partial sums in piece order, kJoinLoads of them in flight: a frequent id's
-// run is hundreds of pieces long, and a warp alone waits for every load (4 in flight: 48 us for
-// 32768 Zipf ids at D = 4096).
+// The runs that cross pieces: their partial sums are added in piece order, kJoinLoads of them in
+// flight, 128 columns at a time: a run of few pieces by a warp; a long one, of a frequent id, by a
+// block, whose warps add an eighth of the pieces each and whose first warp adds those. The runs
+// come from the lists that the sums left, so few blocks suffice and none looks for work (a warp
+// for every piece, joining whatever its run's length: 92 us of 130 for 65536 Zipf ids of 256
+// columns).
 constexpr int kJoinLoads = 8;
+constexpr int kJoinBlocksPerSm = 4;
 
-__global__ void __launch_bounds__(256, 4) grad_join_kernel(const __grid_constant__ GradParams p) {
+__global__ void __launch_bounds__(256, kJoinBlocksPerSm) grad_join_kernel(const __grid_constant__ GradParams p) {
+  __shared__ float4 s_part[8][32];
   pdl_wait();
-  const int chunks = (p.D + 127) / 128;
-  const uint64_t item = static_cast<uint64_t>(blockIdx.x) * 8 + (threadIdx.x >> 5);
-  const int lane = threadIdx.x & 31;
-  const uint32_t piece = static_cast<uint32_t>(item / chunks);
-  const int c = static_cast<int>(item - static_cast<uint64_t>(piece) * chunks) * 128 + lane * 4;
-  const uint64_t k0 = static_cast<uint64_t>(piece) * p.piece, k1 = k0 + p.piece;
-  if (k1 >= p.n) return;
-  const uint32_t key = p.key[k1 - 1];
-  if (key >= p.V || p.key[k1] != key) return;
-  if (p.key[k0] == key && k0 > 0 && p.key[k0 - 1] == key) return;  // it began earlier
-  // the run's last piece: the pieces that begin with its id, 32 at a time, a lane each
-  uint32_t last = piece;
-  for (bool more = true; more;) {
-    const uint64_t at = (static_cast<uint64_t>(last) + 1 + lane) * p.piece;
-    const unsigned in = __ballot_sync(0xffffffffu, at < p.n && p.key[at] == key);
-    more = in == 0xffffffffu;
-    last += more ? 32 : __ffs(~in) - 1;
-  }
-  if (c >= p.D) return;
-  auto partial = [&](uint32_t q, int which) {
+  const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
+  const uint32_t chunks = static_cast<uint32_t>((p.D + 127) / 128);
+  auto partial = [&](uint32_t q, int which, int c) {
     return reinterpret_cast<const float4*>(p.partial + (static_cast<size_t>(q) * 2 + which) * p.D + c);
   };
-  float4 acc = __ldcg(partial(piece, 1));
-  for (uint32_t q0 = piece + 1; q0 <= last; q0 += kJoinLoads) {
-    float4 x[kJoinLoads];
+  auto add = [](float4& a, const float4& b) {
+    a.x += b.x;
+    a.y += b.y;
+    a.z += b.z;
+    a.w += b.w;
+  };
+  // pieces [q0, q1) of a run that began earlier, onto acc
+  auto sum = [&](float4& acc, uint32_t q0, uint32_t q1, int c) {
+    for (uint32_t q = q0; q < q1; q += kJoinLoads) {
+      float4 x[kJoinLoads];
 #pragma unroll
-    for (int k = 0; k < kJoinLoads; ++k)
-      if (q0 + k <= last) x[k] = __ldcg(partial(q0 + k, 0));
+      for (int k = 0; k < kJoinLoads; ++k)
+        if (q + k < q1) x[k] = __ldcg(partial(q + k, 0, c));
 #pragma unroll
-    for (int k = 0; k < kJoinLoads; ++k) {
-      if (q0 + k > last) break;
-      acc.x += x[k].x;
-      acc.y += x[k].y;
-      acc.z += x[k].z;
-      acc.w += x[k].w;
+      for (int k = 0; k < kJoinLoads; ++k)
+        if (q + k < q1) add(acc, x[k]);
     }
+  };
+  // the finished sum of the run that begins in `piece` (its number: that of the next piece's
+  // beginning, which lies in it)
+  auto finish = [&](uint32_t piece, uint32_t key, int c, const float4& acc) {
+    const int64_t row = p.dense ? static_cast<int64_t>(key) : p.piece_run[piece + 1];
+    float4* dst = reinterpret_cast<float4*>(p.out + row * p.D + c);
+    float4 y = make_float4(acc.x * p.scale, acc.y * p.scale, acc.z * p.scale, acc.w * p.scale);
+    if (p.dense) add(y, *dst);
+    *dst = y;
+  };
+  auto key_of = [&](uint32_t piece) { return p.key[static_cast<uint64_t>(piece + 1) * p.piece - 1]; };
+  // pieces after `piece` that begin with its last id, 32 at a time, a lane each
+  auto pieces_after = [&](uint32_t piece, uint32_t key) {
+    uint32_t m = 0;
+    for (bool more = true; more;) {
+      const uint64_t at = (static_cast<uint64_t>(piece) + 1 + m + lane) * p.piece;
+      const unsigned in = __ballot_sync(0xffffffffu, at < p.n && p.key[at] == key);
+      more = in == 0xffffffffu;
+      m += more ? 32 : __ffs(~in) - 1;
+    }
+    return m;
+  };
+  const uint64_t long_items = static_cast<uint64_t>(p.crossing[1]) * chunks;
+  for (uint64_t item = blockIdx.x; item < long_items; item += gridDim.x) {
+    const uint32_t piece = static_cast<uint32_t>(p.lists[p.pieces + item / chunks]);
+    const int c = static_cast<int>(item % chunks) * 128 + lane * 4;
+    const uint32_t key = key_of(piece), m = pieces_after(piece, key);
+    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (c < p.D) {
+      if (w == 0) acc = __ldcg(partial(piece, 1, c));
+      sum(acc, piece + 1 + static_cast<uint32_t>(static_cast<uint64_t>(m) * w / 8),
+          piece + 1 + static_cast<uint32_t>(static_cast<uint64_t>(m) * (w + 1) / 8), c);
+    }
+    s_part[w][lane] = acc;
+    __syncthreads();
+    if (w == 0 && c < p.D) {
+#pragma unroll
+      for (int k = 1; k < 8; ++k) add(acc, s_part[k][lane]);
+      finish(piece, key, c, acc);
+    }
+    __syncthreads();
   }
-  // the run's number: that of the next piece's beginning, which lies in it
-  const int64_t row = p.dense ? static_cast<int64_t>(key) : p.piece_run[piece + 1];
-  float4* dst = reinterpret_cast<float4*>(p.out + row * p.D + c);
-  float4 y = make_float4(acc.x * p.scale, acc.y * p.scale, acc.z * p.scale, acc.w * p.scale);
-  if (p.dense) {
-    const float4 x = *dst;
-    y = make_float4(x.x + y.x, x.y + y.y, x.z + y.z, x.w + y.w);
+  const uint64_t short_items = static_cast<uint64_t>(p.crossing[0]) * chunks;
+  for (uint64_t item = static_cast<uint64_t>(blockIdx.x) * 8 + w; item < short_items; item += static_cast<uint64_t>(gridDim.x) * 8) {
+    const uint32_t piece = static_cast<uint32_t>(p.lists[item / chunks]);
+    const int c = static_cast<int>(item % chunks) * 128 + lane * 4;
+    const uint32_t key = key_of(piece), m = pieces_after(piece, key);
+    if (c >= p.D) continue;
+    float4 acc = __ldcg(partial(piece, 1, c));
+    sum(acc, piece + 1, piece + 1 + m, c);
+    finish(piece, key, c, acc);
   }
-  *dst = y;
 }
 
 // ------------------------------------------------------------------ sort in one cluster
@@ -734,6 +781,7 @@ __global__ void __launch_bounds__(kClusterThreads, 1) sort_cluster_kernel(const 
     }
     if (i < p.n && i % a.r.piece == 0) a.r.piece_run[i / a.r.piece] = static_cast<int32_t>(run) - 1;
   }
+  if (rank == 0 && tid < 2) a.r.crossing[tid] = 0;
   if (a.r.count_out && first) *a.r.count_out = static_cast<int32_t>(all);
 }
 

@@ -261,7 +261,7 @@ int project_mx4(const ngram_embed_plan* p, const HashParams& h, const int32_t* i
 // ---- lookup and gradient of one table ----
 struct GradWs {
   uint32_t *key[2], *counts, *totals, *tile_heads;
-  int32_t *pos[2], *piece_run;
+  int32_t *pos[2], *piece_run, *crossing, *lists;
   float* partial;
   size_t bytes;
 };
@@ -305,7 +305,7 @@ GradWs grad_ws(int64_t n, int64_t D, void* ws) {
   const size_t pieces = static_cast<size_t>(grad_max_pieces(n, D));
   const size_t k0 = take(N * 4), k1 = take(N * 4), p0 = take(N * 4), p1 = take(N * 4);
   const size_t cn = take(tiles << (kSortMaxBits + 2)), to = take(4u << kSortMaxBits), th = take(tiles * 4);
-  const size_t pr = take(pieces * 4), pa = take(pieces * 2 * static_cast<size_t>(D) * 4);
+  const size_t pr = take(pieces * 4), cr = take(8), li = take(pieces * 8), pa = take(pieces * 2 * static_cast<size_t>(D) * 4);
   w.bytes = off;
   if (ws) {
     auto* b = static_cast<uint8_t*>(ws);
@@ -317,6 +317,8 @@ GradWs grad_ws(int64_t n, int64_t D, void* ws) {
     w.totals = reinterpret_cast<uint32_t*>(b + to);
     w.tile_heads = reinterpret_cast<uint32_t*>(b + th);
     w.piece_run = reinterpret_cast<int32_t*>(b + pr);
+    w.crossing = reinterpret_cast<int32_t*>(b + cr);
+    w.lists = reinterpret_cast<int32_t*>(b + li);
     w.partial = reinterpret_cast<float*>(b + pa);
   }
   return w;
@@ -392,6 +394,9 @@ int embedding_bwd(const int32_t* ids, int64_t n, const void* g, int g_dtype, int
   r.chunks = static_cast<int>((D + 255) / 256);
   r.scale = scale;
   r.partial = w.partial;
+  r.crossing = w.crossing;
+  r.lists = w.lists;
+  r.pieces = static_cast<uint32_t>((n + r.piece - 1) / r.piece);
   r.out = out;
   r.dense = dense ? 1 : 0;
   int rc;
@@ -423,13 +428,15 @@ int embedding_bwd(const int32_t* ids, int64_t n, const void* g, int g_dtype, int
     if ((rc = launch(grad_heads_kernel, dim3(r.tiles), dim3(kSortThreads), 0, st, false, 1, r))) return rc;
     if ((rc = launch(grad_number_kernel, dim3(r.tiles), dim3(kSortThreads), 0, st, false, 1, r))) return rc;
   }
-  const int64_t pieces = (n + r.piece - 1) / r.piece;
-  const int64_t items = pieces * r.chunks, join_items = pieces * ((D + 127) / 128);
-  if (join_items > int64_t(INT32_MAX) * 8) return NGRAM_ERR_UNSUPPORTED;
+  const int64_t items = static_cast<int64_t>(r.pieces) * r.chunks;
+  if (items > int64_t(INT32_MAX) * 8) return NGRAM_ERR_UNSUPPORTED;
   const dim3 grid(static_cast<unsigned>((items + 7) / 8));
   rc = g_dtype == NGRAM_BF16 ? launch_grad_reduce<uint16_t>(r, grid, st) : launch_grad_reduce<float>(r, grid, st);
   if (rc) return rc;
-  return launch(grad_join_kernel, dim3(static_cast<unsigned>((join_items + 7) / 8)), dim3(256), 0, st, true, 1, r);
+  // enough for every run that could cross pieces, at most a resident grid
+  const int64_t most = static_cast<int64_t>(r.pieces) * ((D + 127) / 128), resident = int64_t(device_sms()) * kJoinBlocksPerSm;
+  return launch(grad_join_kernel, dim3(static_cast<unsigned>(most < resident ? most : resident)), dim3(256), 0, st, true, 1,
+                r);
 }
 
 dim3 row_map_grid(const RowMap& m) { return dim3((m.items + 7) / 8); }
