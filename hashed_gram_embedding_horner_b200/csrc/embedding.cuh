@@ -543,22 +543,25 @@ __global__ void __launch_bounds__(256, kJoinBlocksPerSm) grad_join_kernel(const 
     *dst = y;
   };
   auto key_of = [&](uint32_t piece) { return p.key[static_cast<uint64_t>(piece + 1) * p.piece - 1]; };
-  // pieces after `piece` that begin with its last id, 32 at a time, a lane each
-  auto pieces_after = [&](uint32_t piece, uint32_t key) {
-    uint32_t m = 0;
-    for (bool more = true; more;) {
-      const uint64_t at = (static_cast<uint64_t>(piece) + 1 + m + lane) * p.piece;
-      const unsigned in = __ballot_sync(0xffffffffu, at < p.n && p.key[at] == key);
-      more = in == 0xffffffffu;
-      m += more ? 32 : __ffs(~in) - 1;
+  // pieces after `piece` that begin with its last id: the lanes look 32 steps ahead at once, of
+  // 1024 pieces each (a long run), then of 32, then of one
+  auto pieces_after = [&](uint32_t piece, uint32_t key, uint32_t stride) {
+    uint64_t m = 0;
+    for (; stride; stride >>= 5) {
+      for (bool more = true; more;) {
+        const uint64_t at = (piece + m + static_cast<uint64_t>(lane + 1) * stride) * p.piece;
+        const unsigned in = __ballot_sync(0xffffffffu, at < p.n && p.key[at] == key);
+        more = in == 0xffffffffu;
+        m += static_cast<uint64_t>(more ? 32 : __ffs(~in) - 1) * stride;
+      }
     }
-    return m;
+    return static_cast<uint32_t>(m);
   };
   const uint64_t long_items = static_cast<uint64_t>(p.crossing[1]) * chunks;
   for (uint64_t item = blockIdx.x; item < long_items; item += gridDim.x) {
     const uint32_t piece = static_cast<uint32_t>(p.lists[p.pieces + item / chunks]);
     const int c = static_cast<int>(item % chunks) * 128 + lane * 4;
-    const uint32_t key = key_of(piece), m = pieces_after(piece, key);
+    const uint32_t key = key_of(piece), m = pieces_after(piece, key, 1024);
     float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
     if (c < p.D) {
       if (w == 0) acc = __ldcg(partial(piece, 1, c));
@@ -578,7 +581,7 @@ __global__ void __launch_bounds__(256, kJoinBlocksPerSm) grad_join_kernel(const 
   for (uint64_t item = static_cast<uint64_t>(blockIdx.x) * 8 + w; item < short_items; item += static_cast<uint64_t>(gridDim.x) * 8) {
     const uint32_t piece = static_cast<uint32_t>(p.lists[item / chunks]);
     const int c = static_cast<int>(item % chunks) * 128 + lane * 4;
-    const uint32_t key = key_of(piece), m = pieces_after(piece, key);
+    const uint32_t key = key_of(piece), m = pieces_after(piece, key, 1);
     if (c >= p.D) continue;
     float4 acc = __ldcg(partial(piece, 1, c));
     sum(acc, piece + 1, piece + 1 + m, c);
