@@ -265,28 +265,35 @@ struct GradWs {
   float* partial;
   size_t bytes;
 };
-// Positions a piece: the longest of 128, 32 and 8 that leaves kGradWarps warps. Long pieces leave
-// few partial sums of the frequent ids to join (32768 Zipf ids at D = 4096, pieces of 16 / 32 /
-// 128: 44 / 22 / JOIN us for the join); short ones have their row loads in flight at once where
-// the warps are few (641 ids of 136 columns, pieces of 32 / 8: 16 / 6 us for the sums).
-constexpr int64_t kGradWarps = 4096;
-constexpr int kGradPieces[3] = {128, 32, 8};
+// Positions a piece: 128 while that leaves 4096 warps, else 32 while that leaves 1024, else 8. Long
+// pieces leave few partial sums of the frequent ids to join, which a run's block adds one after
+// another (65536 Zipf ids over 100 of 256 columns, pieces of 8 / 32: 25 / 8 us for the join); short
+// ones have their row loads in flight at once where the warps are few (641 ids of 136 columns,
+// pieces of 32 / 8: 16 / 6 us for the sums).
+struct GradPiece {
+  int positions;
+  int64_t warps;  // the fewest that it may leave
+};
+constexpr GradPiece kGradPieces[3] = {{128, 4096}, {32, 1024}, {8, 0}};
 int64_t grad_warps(int64_t n, int64_t D, int piece) { return (n + piece - 1) / piece * ((D + 255) / 256); }
 int grad_piece(int64_t n, int64_t D) {
-  for (int k = 0; k < 2; ++k)
-    if (grad_warps(n, D, kGradPieces[k]) >= kGradWarps) return kGradPieces[k];
-  return kGradPieces[2];
+  int k = 0;
+  while (grad_warps(n, D, kGradPieces[k].positions) < kGradPieces[k].warps) ++k;
+  return kGradPieces[k].positions;
 }
-// The most pieces that a call of up to n positions takes (fewer positions may take shorter ones,
-// never more than kGradWarps warps of them).
+// The most pieces that a call of up to n positions takes: fewer positions may take shorter ones,
+// but only while the next longer ones leave too few warps.
 int64_t grad_max_pieces(int64_t n, int64_t D) {
   const int64_t chunks = (D + 255) / 256;
-  int64_t most = (n + kGradPieces[0] - 1) / kGradPieces[0];
-  for (int k = 1; k < 3; ++k) {
-    // pieces of this length: only while the next longer ones are fewer than kGradWarps warps
-    const int64_t longer = kGradPieces[k - 1], limit = (kGradWarps + chunks - 1) / chunks * longer;
-    const int64_t m = ((n < limit ? n : limit) + kGradPieces[k] - 1) / kGradPieces[k];
-    if (m > most) most = m;
+  int64_t most = 0;
+  for (int k = 0; k < 3; ++k) {
+    int64_t m = n;  // positions that take this length
+    if (k) {
+      const int64_t limit = (kGradPieces[k - 1].warps + chunks - 1) / chunks * kGradPieces[k - 1].positions;
+      if (limit < m) m = limit;
+    }
+    const int64_t pieces = (m + kGradPieces[k].positions - 1) / kGradPieces[k].positions;
+    if (pieces > most) most = pieces;
   }
   return most;
 }
