@@ -52,6 +52,7 @@ EXPORTED = [
     "ngram_embed_plan_set_fused_step", "ngram_embed_plan_set_backward_pair",
     "ngram_embed_plan_set_backward_streams",
     "ngram_mx4_scale_bytes", "ngram_mx4_quantize", "ngram_mx4_product_workspace_bytes", "ngram_mx4_product",
+    "ngram_mx4_product_form",
     "ngram_embed_mx4_workspace_bytes", "ngram_embed_fwd_mx4", "ngram_embed_project_mx4",
     "ngram_embedding_workspace_bytes", "ngram_embedding_fwd", "ngram_embedding_bwd", "ngram_embedding_bwd_rows",
 ]
@@ -127,6 +128,7 @@ _sig("ngram_mx4_scale_bytes", [_I64, _I64, ctypes.c_int], _SZ)
 _sig("ngram_mx4_quantize", [_P, ctypes.c_int, _I64, _I64, _I64, _P, _P, ctypes.c_int, _P])
 _sig("ngram_mx4_product_workspace_bytes", [_I64, _I64, _I64], _SZ)
 _sig("ngram_mx4_product", [_MX, _MX, _I64, _I64, _I64, ctypes.c_float, _P, ctypes.c_int, _I64, _P, _SZ, _P])
+_sig("ngram_mx4_product_form", [_I64, _I64, _I64, ctypes.c_int])
 _sig("ngram_embed_mx4_workspace_bytes", [_P, _I64], _SZ)
 _sig("ngram_embed_fwd_mx4", [_P, _P, _P, _I32, _I64, _P, _MX, _MX, _P, _P, _P, _P, _SZ, _P])
 _sig("ngram_embed_project_mx4", [_P, _P, _P, _I64, _P, _MX, _MX, _P, _P, _SZ, _P])
@@ -628,6 +630,13 @@ def ngram_mx4_product(a: Mx4, b: Mx4, out, workspace, alpha: float = 1.0, stream
                                 _stream_of(stream, dev))
     if rc:
         _check(rc, "ngram_mx4_product")
+
+
+def ngram_mx4_product_form(M: int, N: int, K: int, sms: int = 148) -> int:
+    """Columns of the tiles that a product takes on a device of `sms` SMs: 256 (CTA pairs), 192, 128 or 64."""
+    rc = _lib.ngram_mx4_product_form(int(M), int(N), int(K), int(sms))
+    _check(min(rc, 0), "ngram_mx4_product_form")
+    return rc
 
 
 def new_embed_mx4_workspace(plan: Plan, max_tokens: int, device="cuda"):

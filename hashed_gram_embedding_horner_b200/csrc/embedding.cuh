@@ -594,8 +594,9 @@ __global__ void __launch_bounds__(256, kJoinBlocksPerSm) grad_join_kernel(const 
 // Up to kClusterMax positions are sorted and their runs numbered in one launch, by a cluster of
 // CTAs that hold all of them in shared memory: each CTA ranks its positions by digit, the CTAs exchange their digit counts, and every position is stored straight into its
 // place in the shared memory of the CTA that the place belongs to. Positions past n carry the
-// largest key, so they stay last. Measured for 32768 ids below 131072: 13 us, against 45 us of
-// launches and gaps for the tiled sort and the numbering kernels.
+// largest key, so they stay last. The gradient of 1000 / 32768 / 65536 rows of eight columns
+// takes 14 / 31 / 42 us in a graph, against 32 / 45 / 48 with the tiled sort and the numbering
+// kernels, which are ten launches more.
 
 constexpr int kClusterThreads = 1024;
 constexpr int kClusterMaxItems = 4;  // positions a thread: 1, 2 or 4, as few as hold n

@@ -392,7 +392,7 @@ template <int BN, int STAGES, bool PAIR = false>
 struct Mx4Smem {
   static constexpr int kABytes = 128 * 128;
   static constexpr int kBBytes = (PAIR ? BN / 2 : BN) * 128;
-  static constexpr int kSfbRows = BN > 128 ? BN / 128 : 1;  // row blocks of B's scales a tile touches
+  static constexpr int kSfbRows = (BN + 127) / 128;  // row blocks of B's scales a tile touches
   static constexpr int kSfaOffset = kABytes + kBBytes;
   static constexpr int kSfbOffset = kSfaOffset + 2 * kMxTileBytes;
   static constexpr int kStageBytes = kSfbOffset + kSfbRows * 2 * kMxTileBytes;
@@ -586,7 +586,7 @@ __device__ __forceinline__ bool mx4_epilogue(const Mx4GemmParams& p, uint32_t* s
   const bool shares = L::kOverlap && g == (acc ^ 1);
   const int rot = shares && g == 1 ? kChunks - 1 : 0;
   const int row = row0 + lane;
-  auto chunk_col = [&](int cc) { return g * (BN / 2) + ((cc + rot) & (kChunks - 1)) * 32; };
+  auto chunk_col = [&](int cc) { return g * (BN / 2) + (L::kOverlap ? (cc + rot) & (kChunks - 1) : cc) * 32; };
   constexpr int kInFlight = 8 / static_cast<int>(sizeof(OutT));
   constexpr int kDepth = kChunks < kInFlight ? kChunks : kInFlight;  // chunks of E_0 in flight
   Mx4E0<OutT> e[kDepth];
@@ -622,8 +622,8 @@ __device__ __forceinline__ void mx4_issue_stage(uint32_t at, uint32_t tmem_base,
   const uint64_t adesc = sw128_kmajor_desc(at), bdesc = sw128_kmajor_desc(at + L::kABytes);
   const uint64_t da = scale_tile_desc(at + L::kSfaOffset), db = scale_tile_desc(at + L::kSfbOffset);
   const uint32_t sfa = tmem_base + L::kSfaCol;
-  // a tile narrower than a row block of scales starts inside its four columns
-  const uint32_t sfb = tmem_base + L::kSfbCol + (BN < 128 ? static_cast<uint32_t>((col0 & 127) >> 5) : 0u);
+  // a tile that is not whole row blocks of scales may start inside a block's four columns
+  const uint32_t sfb = tmem_base + L::kSfbCol + (BN % 128 ? static_cast<uint32_t>((col0 & 127) >> 5) : 0u);
   // scales of 128 elements of K, then their MMAs of 64
   auto half = [&](int h, bool both) {
     if (PAIR) tmem_cp_scales_pair(sfa + h * 4, da + h * (kMxTileBytes >> 4));

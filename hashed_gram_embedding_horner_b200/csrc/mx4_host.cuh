@@ -153,21 +153,35 @@ int launch_mx4_tiles(Mx4GemmParams prm, const Mx4Operands& o, int sms, cudaStrea
                 prm);
 }
 
-// Which tiles: CTA pairs on 256 x 256, or one CTA on 128 x 128 or 128 x 64. The pairs' tiles
-// bring in the fewest bytes for their products, and a pass of a wave over a k-block takes about
-// 0.42 us, against 0.33 and 0.29 us for the narrower ones; those fill the SMs where the wide
-// ones are too few. Measured on B200, bf16 out (us, wide / 128 / 64): 32768 x 4096 x 4096 206 /
-// 310 / 548, 1280 x 4096 x 4096 17.3 / 20.2 / 28.2, 512 x 4096 x 4096 11.3 / 9.6 / 13.5,
-// 333 x 1111 x 2080 11.6 / 8.7 / 6.6, 128 x 512 x 512 6.8 / 4.7 / 4.0.
+// Which tiles: CTA pairs on 256 x 256 (the fewest bytes for their products), or one CTA on 128 x
+// 192, 128 or 64, whichever finishes its waves first by the times below: a wave of a form costs
+// so many us a k-block and so many besides, and never less than its epilogue. Measured on B200,
+// bf16 out (us, 256 / 192 / 128 / 64; * taken):
+//   32768 x 2048 x 2048   61.5* 72.4  82.9 150.4     1280 x 4096 x 4096  17.0  15.8* 18.5  27.2
+//    4096 x 4096 x 4096   28.7* 33.8  39.3  71.4     1280 x 2048 x 2048   8.6   6.6*  8.7  10.4
+//    8192 x 2048 x 2048   18.9* 19.6  22.9  39.7      512 x 4096 x 4096  11.0   9.2   8.4* 12.6
+//    5000 x 8192 x 320    30.2* 32.6  35.6  47.3      333 x 1111 x 2080  11.5  10.1   8.3   6.2*
+//   16384 x 1000 x 512    17.1  17.7  16.4* 19.5        1 x 4096 x 4096  10.0   8.4   7.6   7.2*
+struct Mx4Form {
+  int rows, cols;              // of a tile
+  double us_kb, us_tile, least, once;  // a wave's us: for a k-block, besides, at least; the call's besides
+};
+constexpr Mx4Form kMx4Forms[4] = {
+    {256, 256, 0.32, 1.6, 3.1, 1.5}, {128, 192, 0.30, 1.3, 2.5, 0.0}, {128, 128, 0.26, 1.0, 1.75, 0.0}, {128, 64, 0.27, 0.5, 1.25, 0.0}};
 int mx4_tile_width(int M, int N, int K, int sms) {
-  const double kb = (K + 255) / 256;
-  auto cost = [&](int rows, int cols, int workers, double us_kb, double us_tile) {
-    const int64_t tiles = (static_cast<int64_t>(M) + rows - 1) / rows * ((static_cast<int64_t>(N) + cols - 1) / cols);
-    return static_cast<double>((tiles + workers - 1) / workers) * (kb * us_kb + us_tile);
-  };
-  const double wide = cost(256, 256, sms / 2, 0.42, 1.6), mid = cost(128, 128, sms, 0.33, 1.0),
-               narrow = cost(128, 64, sms, 0.29, 0.5);
-  return wide <= mid && wide <= narrow ? 256 : (mid <= narrow ? 128 : 64);
+  int width = 0;
+  double best = 0;
+  for (const Mx4Form& f : kMx4Forms) {
+    const int64_t tiles = (static_cast<int64_t>(M) + f.rows - 1) / f.rows * ((static_cast<int64_t>(N) + f.cols - 1) / f.cols);
+    const int64_t workers = sms * 128 / f.rows, waves = (tiles + workers - 1) / workers;
+    const double wave = (K + 255) / 256 * f.us_kb + f.us_tile;
+    const double us = f.once + static_cast<double>(waves) * (wave > f.least ? wave : f.least);
+    if (!width || us < best) {
+      width = f.cols;
+      best = us;
+    }
+  }
+  return width;
 }
 
 template <typename OutT>
@@ -175,6 +189,7 @@ int launch_mx4_gemm(const Mx4GemmParams& prm, const Mx4Operands& o, int sms, cud
   if (sms < 2) return NGRAM_ERR_CUDA;
   switch (mx4_tile_width(prm.M, prm.N, prm.K, sms)) {
     case 256: return launch_mx4_tiles<256, 5, OutT, true>(prm, o, sms, st);
+    case 192: return launch_mx4_tiles<192, 5, OutT, false>(prm, o, sms, st);
     case 128: return launch_mx4_tiles<128, 6, OutT, false>(prm, o, sms, st);
     default: return launch_mx4_tiles<64, 8, OutT, false>(prm, o, sms, st);
   }
@@ -524,6 +539,12 @@ int ngram_mx4_quantize(const void* src, int dtype, int64_t rows, int64_t cols, i
     if (rc) return rc;
   }
   return NGRAM_OK;
+}
+
+int ngram_mx4_product_form(int64_t M, int64_t N, int64_t K, int sms) {
+  if (M < 1 || M > INT32_MAX - 256 || N < 1 || N > INT32_MAX - 256 || K < 1 || K > INT32_MAX - 256 || sms < 2)
+    return NGRAM_ERR_INVALID_ARG;
+  return mx4_tile_width(static_cast<int>(M), static_cast<int>(N), static_cast<int>(K), sms);
 }
 
 size_t ngram_mx4_product_workspace_bytes(int64_t M, int64_t N, int64_t K) {

@@ -351,7 +351,7 @@ size_t ngram_mx4_scale_bytes(int64_t rows, int64_t cols, int layout);
  *   e    = clamp(floor(log2(max |x| of the block)) - 2 + 127, 0, 254), 0 for a block of zeros;
  *   code = x / 2^(e - 127) rounded to the nearest E2M1 value, ties to even, saturating at 6.
  * A block that holds an infinity or a NaN becomes NaN: e = 255, codes 0. cols must be a
- * multiple of 32 (else NGRAM_ERR_UNSUPPORTED). src is read fastest when it is 16-byte aligned
+ * multiple of 32 (else NGRAM_ERR_UNSUPPORTED). codes and scales are 16-byte aligned. src is read fastest when it is 16-byte aligned
  * and its rows' stride is a multiple of 16 bytes; element alignment is enough. */
 int ngram_mx4_quantize(const void* src, int dtype, int64_t rows, int64_t cols, int64_t src_stride,
                        void* codes, void* scales, int layout, void* stream);
@@ -366,6 +366,11 @@ size_t ngram_mx4_product_workspace_bytes(int64_t M, int64_t N, int64_t K);
 int ngram_mx4_product(const ngram_mx4* A, const ngram_mx4* B, int64_t M, int64_t N, int64_t K,
                       float alpha, void* out, int out_dtype, int64_t out_stride, void* workspace,
                       size_t workspace_bytes, void* stream);
+
+/* The tiles that a product of these sizes takes on a device of `sms` SMs (the layer on 4-bit
+ * tables: M tokens, N = K = D, the plan's SM count): 256 = CTA pairs on 256 x 256 tiles; 192, 128
+ * or 64 = one CTA on 128 rows x that many columns. Negative on bad arguments. */
+int ngram_mx4_product_form(int64_t M, int64_t N, int64_t K, int sms);
 
 /* The whole layer (Eq. 2 + Eq. 3) with 4-bit sub-tables and a 4-bit projection:
  *   E_nk  HOST array of S tables [V_nk[s] x d], scales by rows

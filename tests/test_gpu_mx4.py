@@ -89,6 +89,8 @@ def test_quantising_what_a_quantised_row_stands_for_changes_nothing(ne):
 @pytest.mark.parametrize("M,N,K", [
     (1, 1, 32), (1, 16, 64), (5, 7, 96), (2, 64, 128), (128, 128, 256), (129, 257, 288), (127, 65, 320), (64, 192, 512),
     (33, 4096, 1024), (300, 1000, 2080), (640, 512, 4096), (1, 2048, 4096), (2000, 1536, 544),
+    (600, 2048, 1056), (2300, 2048, 320), (2200, 2100, 96), (1290, 2047, 544), (700, 2500, 64), (3024, 5774, 64),
+    (6864, 2528, 96), (2290, 2048, 1056), (2300, 2041, 2048),
 ])
 def test_product_within_the_bound_of_its_sums(ne, M, N, K, out_dtype):
     rng = np.random.default_rng(M * 7 + N * 3 + K)
@@ -100,6 +102,12 @@ def test_product_within_the_bound_of_its_sums(ne, M, N, K, out_dtype):
     assert ne.ngram_embed_get_status(ws) == 0
     want = av @ bv.T * 0.5
     assert (np.abs(f64(out) - want) <= ref.product_bound(av, bv * 0.5, HALF[out_dtype], want)).all()
+
+
+def test_products_above_take_every_form_of_tiles(ne):
+    sizes = [m.args[1] for m in test_product_within_the_bound_of_its_sums.pytestmark
+             if m.name == "parametrize" and m.args[0] == "M,N,K"][0]
+    assert {ne.ngram_mx4_product_form(*s) for s in sizes} == {64, 128, 192, 256}
 
 
 @pytest.mark.parametrize("out_dtype", [BF16, F32])
@@ -187,11 +195,11 @@ def test_layer_from_4bit_tables(ne, case, lengths):
 
 @pytest.mark.parametrize("dtype,D,N,K,lengths", [
     (BF16, 1024, 3, 1, [3000, 0, 1, 700, 299]), (F32, 1024, 3, 1, [3999]), (BF16, 1056, 4, 1, [2049, 2048]),
-    (BF16, 1280, 5, 2, [1] * 3000),
+    (BF16, 1280, 5, 2, [1] * 3000), (BF16, 2048, 3, 2, [2300]), (F32, 2048, 3, 2, [1, 2299]), (BF16, 2080, 2, 1, [1200, 101]),
 ])
 def test_layer_of_many_tokens(ne, dtype, D, N, K, lengths):
-    """Enough rows for the widest tiles, whose kernel gathers its rows itself; twice on one
-    workspace (its counters come back to zero), and once with ids out of range."""
+    """Several tiles a CTA, in every form of them; twice on one workspace, then with ids out of
+    range, then with bad offsets."""
     S = (N - 1) * K
     V0, V = 5000, [3001 + 10 * s for s in range(S)]
     L = make_layer(ne, D, V0, D, N, K, V, dtype)
@@ -210,7 +218,7 @@ def test_layer_of_many_tokens(ne, dtype, D, N, K, lengths):
         assert ne.ngram_embed_get_status(ws) == (0x1 if bad else 0)
         want, acc, idx = ref.layer(V0, N, K, V, good, off, f64(L["E0"]), L["E_vals"], L["W_vals"])
         assert (np.abs(f64(out) - want) <= acc + HALF[dtype] * (np.abs(want) + acc)).all()
-    assert not bool(ws[256:33024].any())
+    assert not bool(ws[256:33024].any())  # the counters of other calls stay zero
     ne.ngram_embed_clear_status(ws)
     again = torch.empty_like(out)
     ne.ngram_embed_project_mx4(L["plan"], torch.from_numpy(good).cuda(), torch.from_numpy(idx.astype(np.int32)).cuda(),

@@ -69,6 +69,22 @@ def test_product_refusals(ne):
     assert f(M=0) == 0 and f(N=0, ld=0) == 0
 
 
+@pytest.mark.parametrize("M,N,K,sms,form", [
+    (32768, 2048, 2048, 148, 256), (65536, 4096, 4096, 148, 256), (2300, 2048, 2048, 148, 256),  # 72 of 74 pairs' tiles
+    (1280, 4096, 4096, 148, 192), (1280, 2048, 2048, 148, 192), (512, 4096, 4096, 148, 128), (333, 1111, 2080, 148, 64),
+    (1, 4096, 4096, 148, 64), (1, 1, 32, 2, 64), (1280, 4096, 4096, 40, 256),
+])
+def test_product_tiles_for_a_device_size(ne, M, N, K, sms, form):
+    assert ne.ngram_mx4_product_form(M, N, K, sms) == form
+
+
+def test_product_form_refusals(ne):
+    for bad in ((0, 1, 32, 148), (1, 0, 32, 148), (1, 1, 0, 148), (1, 1, 32, 1), (1 << 31, 1, 32, 148)):
+        assert ne._lib.ngram_mx4_product_form(*bad) == -1
+        with pytest.raises(ne.NgramError):
+            ne.ngram_mx4_product_form(*bad)
+
+
 def _plan(ne, V0=1000, D=128, N=3, K=2, V=(11, 13, 17, 19), dtype=0):
     return ne.ngram_embed_plan_create(V0, D, N, K, V, dtype)
 
