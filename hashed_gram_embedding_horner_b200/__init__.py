@@ -561,6 +561,8 @@ def _ids(t, name, device, n=None):
 
 def _space(workspace, device):
     """A workspace's address and bytes."""
+    if workspace is None or not workspace.is_contiguous():
+        raise NgramError("workspace must be a contiguous CUDA tensor")
     _on(device, "workspace", workspace)
     return workspace.data_ptr(), workspace.numel() * workspace.element_size()
 

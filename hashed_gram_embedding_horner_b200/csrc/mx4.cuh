@@ -66,8 +66,8 @@ struct RowMap {
   __host__ static int unroll(uint32_t vecs) { return vecs >= 128 ? 4 : (vecs >= 64 ? 2 : 1); }
 };
 
-// A lane's part of warp `item`: rows row[0 .. 4/U) (a row past the last is not `on`), and its
-// first vector of a row; vector u is vec + u * stride.
+// A lane's part of its warp's item: rows row0 + r * row_step, r < 4 / U, and vectors vec + u *
+// stride of each; either may lie past the last.
 template <int U>
 struct RowPart {
   static constexpr int R = 4 / U;
@@ -387,7 +387,6 @@ constexpr int kMxThreads = 128 + 32 * kMxEpiWarps;  // warp 0 loads, warp 1 MMA 
 
 // PAIR: CTA pairs, 256 x BN tiles; each CTA holds its 128 rows of A with their scales, half of
 // B's rows, and the scales of all of B's rows.
-
 template <int BN, int STAGES, bool PAIR = false>
 struct Mx4Smem {
   static constexpr int kABytes = 128 * 128;
@@ -596,7 +595,10 @@ __device__ __forceinline__ bool mx4_epilogue(const Mx4GemmParams& p, uint32_t* s
 #pragma unroll
   for (int cc = 0; cc < kDepth; ++cc) load_e(cc, col0 + chunk_col(cc));
   if (!ready()) return false;
-  if (L::kOverlap && !shares) release();
+  if (L::kOverlap && !shares) {
+    tc_fence_before();  // this warp's reads of the tile before
+    release();
+  }
   const uint32_t taddr = tmem_base + (static_cast<uint32_t>(q * 32) << 16) + static_cast<uint32_t>(acc * L::kAccStride);
 #pragma unroll
   for (int cc = 0; cc < kChunks; ++cc) {

@@ -351,8 +351,9 @@ size_t ngram_mx4_scale_bytes(int64_t rows, int64_t cols, int layout);
  *   e    = clamp(floor(log2(max |x| of the block)) - 2 + 127, 0, 254), 0 for a block of zeros;
  *   code = x / 2^(e - 127) rounded to the nearest E2M1 value, ties to even, saturating at 6.
  * A block that holds an infinity or a NaN becomes NaN: e = 255, codes 0. cols must be a
- * multiple of 32 (else NGRAM_ERR_UNSUPPORTED). codes and scales are 16-byte aligned. src is read fastest when it is 16-byte aligned
- * and its rows' stride is a multiple of 16 bytes; element alignment is enough. */
+ * multiple of 32 (else NGRAM_ERR_UNSUPPORTED). codes and scales are 16-byte aligned. src is
+ * read fastest when it is 16-byte aligned and its rows' stride is a multiple of 16 bytes;
+ * element alignment is enough. The call's device is the one that owns codes. */
 int ngram_mx4_quantize(const void* src, int dtype, int64_t rows, int64_t cols, int64_t src_stride,
                        void* codes, void* scales, int layout, void* stream);
 
@@ -361,7 +362,7 @@ int ngram_mx4_quantize(const void* src, int dtype, int64_t rows, int64_t cols, i
  * NGRAM_F32). out has a row stride of out_stride elements (any; 16-byte aligned rows are
  * written fastest). K must be a multiple of 32.
  *   workspace  >= ngram_mx4_product_workspace_bytes(M, N, K); its head as for a plan's
- *              workspace (zeroed once; status word) */
+ *              workspace (zeroed once; status word). The device that owns it is the call's. */
 size_t ngram_mx4_product_workspace_bytes(int64_t M, int64_t N, int64_t K);
 int ngram_mx4_product(const ngram_mx4* A, const ngram_mx4* B, int64_t M, int64_t N, int64_t K,
                       float alpha, void* out, int out_dtype, int64_t out_stride, void* workspace,
@@ -397,14 +398,15 @@ int ngram_embed_project_mx4(const ngram_embed_plan* plan, const int32_t* tokens,
 /* ---- one table: lookup and gradient ----
  * out[i] = scale * table[ids[i]] for n int32 ids (device), in fp32, rounded once to out_dtype.
  *   table        [V x D] NGRAM_BF16, NGRAM_F32, or NGRAM_MX4 codes with table_scales by rows
- *                (NULL otherwise); D a multiple of 8 (NGRAM_MX4: of 32)
+ *                (NULL otherwise), 16-byte aligned; D a multiple of 8 (NGRAM_MX4: of 32)
  *   ids          NULL: ids[i] = i, n <= V (a whole table read back)
  *   pad_id       positions whose id is pad_id get a row of zeros and the gradient skips them;
  *                negative: none
  *   out          [n x D] NGRAM_BF16 or NGRAM_F32, row stride out_stride elements (rows and base
  *                16-byte aligned)
- *   workspace    >= ngram_embedding_workspace_bytes(0, D): the status word's head. An id outside
- *                [0, V) reads row 0 and sets NGRAM_STATUS_BAD_TOKEN. */
+ *   workspace    >= ngram_embedding_workspace_bytes(0, D): the status word's head; the device
+ *                that owns it is the call's. An id outside [0, V) that is not pad_id reads row 0
+ *                and sets NGRAM_STATUS_BAD_TOKEN. */
 size_t ngram_embedding_workspace_bytes(int64_t max_ids, int64_t D);
 int ngram_embedding_fwd(const void* table, const void* table_scales, int table_dtype, int64_t V,
                         int64_t D, const int32_t* ids, int64_t n, float scale, int64_t pad_id,
@@ -412,10 +414,11 @@ int ngram_embedding_fwd(const void* table, const void* table_scales, int table_d
                         size_t workspace_bytes, void* stream);
 
 /* Its gradient: d_table[v] += scale * sum of grad_out[i] over the positions i with ids[i] = v
- * (d_table [V x D] fp32). grad_out is [n x D] NGRAM_BF16 or NGRAM_F32, row stride grad_stride
- * elements. Positions are sorted by id and summed in fp32 in a fixed order without atomics:
- * equal inputs give equal bits. For a 4-bit table this is the gradient of its master (the
- * straight-through estimate). Ids outside [0, V) count as row 0, as in the lookup.
+ * (d_table [V x D] fp32, D a multiple of 8). grad_out is [n x D] NGRAM_BF16 or NGRAM_F32, row
+ * stride grad_stride elements. Rows of grad_out and the gradients are 16-byte aligned. Positions
+ * are sorted by id and summed in fp32 in a fixed order without atomics: equal inputs give equal
+ * bits. For a 4-bit table this is the gradient of its master (the straight-through estimate).
+ * Ids outside [0, V) count as row 0, as in the lookup.
  *   workspace  >= ngram_embedding_workspace_bytes(n, D) */
 int ngram_embedding_bwd(const int32_t* ids, int64_t n, const void* grad_out, int grad_dtype,
                         int64_t grad_stride, int64_t V, int64_t D, float scale, int64_t pad_id,

@@ -259,3 +259,57 @@ def test_gradient_captured_and_replayed(ne):
         U = int(count)
         assert np.array_equal(rows[:U].cpu().numpy(), want_rows)
         assert (np.abs(f64(grads[:U]) - want) <= ref.grad_bound(mags, cnt)).all()
+
+
+def test_on_other_streams_at_once(ne):
+    """The current stream of a `with` block and a given one, each with its own workspace: lookups
+    and gradients, sorted in one cluster and in tiles, beside one another give the bits of a call
+    alone."""
+    rng = np.random.default_rng(31)
+    V, D = 4000, 72
+    sizes = (3000, 70000)
+    table = torch.from_numpy(rng.standard_normal((V, D))).float().cuda()
+    ins = []
+    for n in sizes:
+        ids = torch.from_numpy(ids_of(rng, n, V, "zipf")).cuda()
+        ins.append((ids, torch.from_numpy(rng.standard_normal((n, D))).float().cuda()))
+
+    def call(k, st=None):
+        ids, g = ins[k]
+        out, d, ws = torch.empty_like(g), torch.zeros((V, D), device="cuda"), ne.new_embedding_workspace(sizes[k], D)
+        torch.cuda.synchronize()  # allocated and cleared before another stream takes them
+        ne.ngram_embedding_fwd(table, ids, out, ws, scale=1.5, pad_id=1, stream=st)
+        ne.ngram_embedding_bwd(ids, g, d, ws, scale=1.5, pad_id=1, stream=st)
+        return out, d
+
+    alone = [call(k) for k in range(2)]
+    for _ in range(3):
+        given = torch.cuda.Stream()
+        with torch.cuda.stream(torch.cuda.Stream()):
+            both = [call(0, given), call(1)]
+        torch.cuda.synchronize()
+        for got, want in zip(both, alone):
+            assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+
+
+@pytest.mark.parametrize("pad_id", [0, 49, 50, 1 << 40])
+def test_padding_at_the_table_s_edges(ne, pad_id):
+    """A pad id of the first, the last and no row; an id past the table that is the pad id is
+    padding, any other reads row 0 (a row of its own even where 0 is the pad id)."""
+    rng = np.random.default_rng(32)
+    n, V, D = 600, 50, 40
+    ids = rng.integers(0, V + 2, n).astype(np.int32)
+    table = rng.integers(-64, 65, (V, D)).astype(np.float32)
+    g = rng.integers(-16, 17, (n, D)).astype(np.float32)
+    ws = ne.new_embedding_workspace(n, D)
+    ids_d, out = torch.from_numpy(ids).cuda(), torch.full((n, D), 9.0, device="cuda")
+    d = torch.zeros((V, D), device="cuda")
+    ne.ngram_embedding_fwd(torch.from_numpy(table).cuda(), ids_d, out, ws, pad_id=pad_id)
+    ne.ngram_embedding_bwd(ids_d, torch.from_numpy(g).cuda(), d, ws, pad_id=pad_id)
+    assert ne.ngram_embed_get_status(ws) == 0x1
+    pad = ids == pad_id
+    row = np.where(ids < V, ids, 0)
+    want = np.zeros((V, D))
+    np.add.at(want, row[~pad], g[~pad].astype(np.float64))
+    assert np.array_equal(f64(out), np.where(pad[:, None], 0.0, table[row]))
+    assert np.array_equal(f64(d), want)  # sums of at most 600 integers below 17: exact

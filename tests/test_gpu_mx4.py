@@ -334,3 +334,70 @@ def test_captured_replayed_and_on_another_stream(ne):
         av, bv = ref.values(*ref.quantise(f64(x))), ref.values(*w)
         want = av @ bv.T
         assert (np.abs(f64(out) - want) <= ref.product_bound(av, bv, ref.F32_HALF, want)).all()
+
+
+def test_captured_behind_copies_and_across_two_streams(ne):
+    """One graph: inputs copied and outputs cleared by copy and memset nodes, W and x quantised on
+    two streams, joined in front of the product, which a lookup of the quantised rows follows."""
+    M, N, K = 70, 160, 96
+    xs, ws_ = torch.empty((M, K)).pin_memory(), torch.empty((N, K)).pin_memory()
+    x, w = torch.empty((M, K), device="cuda"), torch.empty((N, K), device="cuda")
+    a, b, rows = ne.Mx4.empty(M, K, ne.MX4_TILES), ne.Mx4.empty(N, K, ne.MX4_TILES), ne.Mx4.empty(M, K)
+    out, back = torch.empty((M, N), device="cuda"), torch.empty((M, K), device="cuda")
+    ws, ws2 = ne.new_mx4_workspace(M, N, K), ne.new_embedding_workspace(0, K)
+    side = torch.cuda.Stream()
+
+    def step():
+        main = torch.cuda.current_stream()
+        x.copy_(xs, non_blocking=True)
+        side.wait_stream(main)
+        with torch.cuda.stream(side):
+            w.copy_(ws_, non_blocking=True)
+            ne.ngram_mx4_quantize(w, b)
+        ne.ngram_mx4_quantize(x, a)
+        ne.ngram_mx4_quantize(x, rows)
+        out.zero_()
+        main.wait_stream(side)
+        ne.ngram_mx4_product(a, b, out, ws)
+        back.zero_()
+        ne.ngram_embedding_fwd(rows, None, back, ws2)
+
+    with torch.cuda.stream(torch.cuda.Stream()):
+        step()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        step()
+    rng = np.random.default_rng(40)
+    for k in range(3):
+        xs.copy_(torch.from_numpy(rng.standard_normal((M, K)) * (k + 1)))
+        ws_.copy_(torch.from_numpy(rng.standard_normal((N, K))))
+        graph.replay()
+        torch.cuda.synchronize()
+        av, bv = (ref.values(*ref.quantise(f64(t))) for t in (xs, ws_))
+        want = av @ bv.T
+        assert (np.abs(f64(out) - want) <= ref.product_bound(av, bv, ref.F32_HALF, want)).all()
+        assert np.array_equal(f64(back), av)
+
+
+def test_products_of_every_form_at_once_on_two_streams(ne):
+    """Two streams run products of different forms beside one another, with their own
+    workspaces: each result has the bits of its call alone."""
+    rng = np.random.default_rng(41)
+    calls = []
+    for M, N, K in ((2000, 1536, 256), (1280, 1024, 256), (700, 520, 320), (1, 640, 96)):
+        a, b = (device_mx4(ne, *ref.random_mx4(rng, r, K), ne.MX4_TILES) for r in (M, N))
+        out, ws = torch.empty((M, N), dtype=BF16, device="cuda"), ne.new_mx4_workspace(M, N, K)
+        ne.ngram_mx4_product(a, b, out, ws)
+        calls.append((a, b, out.clone(), [(torch.empty_like(out), ne.new_mx4_workspace(M, N, K)) for _ in range(2)]))
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    for _ in range(20):
+        for k in range(len(calls)):
+            for i, st in enumerate(streams):
+                a, b, _, own = calls[(k + i * 2) % len(calls)]
+                ne.ngram_mx4_product(a, b, *own[i], stream=st)
+    torch.cuda.synchronize()
+    for _, _, want, own in calls:
+        for out, ws in own:
+            assert torch.equal(out, want) and ne.ngram_embed_get_status(ws) == 0

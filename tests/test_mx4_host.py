@@ -162,3 +162,6 @@ def test_binding_refuses_host_tensors_and_wrong_shapes(ne):
     with pytest.raises(ne.NgramError):
         ne.ngram_embedding_bwd_rows(torch.zeros(4, dtype=torch.int32), cpu, 4, torch.zeros(4, dtype=torch.int32),
                                     torch.zeros(1, dtype=torch.int32), cpu, cpu)
+    for none in (None, torch.zeros(64, dtype=torch.uint8)[::2]):
+        with pytest.raises(ne.NgramError):
+            ne._space(none, -1)
