@@ -354,7 +354,8 @@ __global__ void __launch_bounds__(kMx4GatherThreads) mx4_gather_kernel(const __g
 // thread in front of the stage's MMAs; the tensor pipe keeps their order.
 struct Mx4Maps {
   CUtensorMap A;   // [M x K / 2] bytes, box 128 x 128 rows
-  CUtensorMap B;   // [N x K / 2] bytes, box 128 x BN rows (pairs: BN / 2)
+  CUtensorMap B;   // [N x K / 2] bytes, box 128 x the rows of a CTA's first part of B
+  CUtensorMap B1;  // of its second part
   CUtensorMap At;  // boxes of the rows that the last box of A or B holds, to a multiple of 8:
   CUtensorMap Bt;  // a box with many rows past the array's end takes far longer to fill
   CUtensorMap SA;  // scale tiles as [row blocks x kt * 128] words, box 256 words (two tiles) x 1
@@ -386,10 +387,22 @@ constexpr int kMxStageWords = 32 * 9;  // of shared memory an epilogue warp: 32 
 constexpr int kMxThreads = 128 + 32 * kMxEpiWarps;  // warp 0 loads, warp 1 MMA and TMEM, warps 4-11 epilogue
 
 // PAIR: CTA pairs, 256 x BN tiles; each CTA holds its 128 rows of A with their scales, half of
-// B's rows, and the scales of all of B's rows.
+// B's rows, and the scales of all of B's rows. Tiles wider than an instruction (256 columns) are
+// computed in parts side by side, of which each CTA of a pair holds half.
 template <int BN, int STAGES, bool PAIR = false>
 struct Mx4Smem {
   static constexpr int kABytes = 128 * 128;
+  static constexpr int kParts = BN > 256 ? 2 : 1;
+  __host__ __device__ static constexpr int part_n(int part) {
+    const int n0 = BN > 256 ? (BN / 2 + 63) / 64 * 64 : BN;
+    return part ? BN - n0 : n0;
+  }
+  // scale_vec::2X takes scales from an even column on, of 32 rows each
+  static_assert(BN % 64 == 0 && part_n(0) <= 256, "parts begin at an even column of scales");
+  __host__ __device__ static constexpr int part_rows(int part) { return PAIR ? part_n(part) / 2 : part_n(part); }  // in a CTA
+  // first row of CTA `rank`'s part of a tile's rows of B
+  __host__ __device__ static constexpr int part_row(int part, int rank) { return part * part_n(0) + rank * part_rows(part); }
+  static constexpr int kPartOffset = part_rows(0) * 128;  // of part 1
   static constexpr int kBBytes = (PAIR ? BN / 2 : BN) * 128;
   static constexpr int kSfbRows = (BN + 127) / 128;  // row blocks of B's scales a tile touches
   static constexpr int kSfaOffset = kABytes + kBBytes;
@@ -400,12 +413,14 @@ struct Mx4Smem {
   static constexpr int kStgOffset = (kBarOffset + kNumBars * 8 + 16 + 15) / 16 * 16;
   static constexpr int kBytes = kStgOffset + kMxEpiWarps * kMxStageWords * 4;
   static constexpr int kLaunchBytes = kBytes + 1024;
-  static_assert(kStageBytes % 1024 == 0, "swizzled tiles start on 1024-byte boundaries");
+  static_assert(kStageBytes % 1024 == 0 && kPartOffset % 1024 == 0, "swizzled tiles start on 1024-byte boundaries");
   // TMEM: two accumulators and the stage's scales. At BN = 256 the accumulators share 32
   // columns ([224, 256)), which leaves 32 for the scales: the epilogue drains the shared
-  // columns first and hands them over, so the next tile's MMAs still overlap the drain.
+  // columns first and hands them over, so the next tile's MMAs still overlap the drain. Wider
+  // tiles have one accumulator.
   static constexpr bool kOverlap = BN == 256;
-  static constexpr int kAccStride = kOverlap ? 224 : BN;
+  static constexpr int kAccs = BN > 256 ? 1 : 2;
+  static constexpr int kAccStride = kAccs == 1 ? 0 : (kOverlap ? 224 : BN);
   static constexpr int kSfaCol = kAccStride + BN;
   static constexpr int kSfbCol = kSfaCol + 8;
   static constexpr int kTmemCols = kSfbCol + kSfbRows * 8 <= 256 ? 256 : 512;
@@ -620,7 +635,6 @@ __device__ __forceinline__ bool mx4_epilogue(const Mx4GemmParams& p, uint32_t* s
 template <typename L, int BN, bool PAIR>
 __device__ __forceinline__ void mx4_issue_stage(uint32_t at, uint32_t tmem_base, int col0, uint32_t d_tmem, int left,
                                                 bool first) {
-  constexpr uint32_t idesc0 = umma_idesc_mx4(PAIR ? 256 : 128, BN, 0), idesc1 = umma_idesc_mx4(PAIR ? 256 : 128, BN, 2);
   const uint64_t adesc = sw128_kmajor_desc(at), bdesc = sw128_kmajor_desc(at + L::kABytes);
   const uint64_t da = scale_tile_desc(at + L::kSfaOffset), db = scale_tile_desc(at + L::kSfbOffset);
   const uint32_t sfa = tmem_base + L::kSfaCol;
@@ -639,10 +653,16 @@ __device__ __forceinline__ void mx4_issue_stage(uint32_t at, uint32_t tmem_base,
 #pragma unroll
     for (int k = 0; k < 2; ++k) {
       if (k == 1 && !both) break;
-      const uint32_t fb = sfb + h * L::kSfbRows * 4, more = !first || h != 0 || k != 0 ? 1u : 0u;
-      const uint64_t ka = adesc + 2u * (2 * h + k), kbd = bdesc + 2u * (2 * h + k);
-      if (PAIR) umma_mx4_pair(d_tmem, ka, kbd, k ? idesc1 : idesc0, sfa + h * 4, fb, more);
-      else umma_mx4(d_tmem, ka, kbd, k ? idesc1 : idesc0, sfa + h * 4, fb, more);
+      const uint32_t more = !first || h != 0 || k != 0 ? 1u : 0u;
+      const uint64_t ka = adesc + 2u * (2 * h + k);
+#pragma unroll
+      for (int part = 0; part < L::kParts; ++part) {
+        const uint32_t idesc = umma_idesc_mx4(PAIR ? 256 : 128, L::part_n(part), 2 * k);
+        const uint32_t d = d_tmem + part * L::part_n(0), fb = sfb + h * L::kSfbRows * 4 + part * (L::part_n(0) / 32);
+        const uint64_t kbd = bdesc + 2u * (2 * h + k) + part * (L::kPartOffset >> 4);
+        if (PAIR) umma_mx4_pair(d, ka, kbd, idesc, sfa + h * 4, fb, more);
+        else umma_mx4(d, ka, kbd, idesc, sfa + h * 4, fb, more);
+      }
     }
   };
   if (left >= 256) {
@@ -698,6 +718,7 @@ __global__ void __launch_bounds__(kMxThreads, 1)
   if (warp == 0 && lane == 0) {
     tma_prefetch_desc(&maps.A);
     tma_prefetch_desc(&maps.B);
+    if (L::kParts > 1) tma_prefetch_desc(&maps.B1);
     tma_prefetch_desc(&maps.At);
     tma_prefetch_desc(&maps.Bt);
     tma_prefetch_desc(&maps.SA);
@@ -734,14 +755,22 @@ __global__ void __launch_bounds__(kMxThreads, 1)
       bool ok = true;
       for (int tile = worker; tile < num_tiles && ok; tile += workers) {
         const int m_blk = (tile / p.num_n_blocks) * kRanks + static_cast<int>(rank), n_blk = tile % p.num_n_blocks;
-        constexpr int kBRows = PAIR ? BN / 2 : BN;
-        const int brow = n_blk * BN + static_cast<int>(rank) * kBRows;
-        const int a_rows = mx4_box_rows(p.M, m_blk * 128, 128), b_rows = mx4_box_rows(p.N, brow, kBRows);
+        const int a_rows = mx4_box_rows(p.M, m_blk * 128, 128);
         const void* map_a = a_rows == 128 ? &maps.A : &maps.At;
-        const void* map_b = b_rows == kBRows ? &maps.B : &maps.Bt;
-        uint32_t tx = kRanks * (L::kStageBytes - L::kABytes - L::kBBytes) + (a_rows + b_rows) * 128;
-        if (PAIR)  // rank 0 posts the bytes of both
-          tx += (mx4_box_rows(p.M, m_blk * 128 + 128, 128) + mx4_box_rows(p.N, brow + kBRows, kBRows)) * 128;
+        uint32_t tx = kRanks * (L::kStageBytes - L::kABytes - L::kBBytes) + a_rows * 128;
+        if (PAIR) tx += mx4_box_rows(p.M, m_blk * 128 + 128, 128) * 128;  // rank 0 posts the bytes of both
+        int brow[L::kParts], b_rows[L::kParts];
+#pragma unroll
+        for (int part = 0; part < L::kParts; ++part) {
+          const int kRows = L::part_rows(part);
+          brow[part] = n_blk * BN + L::part_row(part, static_cast<int>(rank));
+          b_rows[part] = mx4_box_rows(p.N, brow[part], kRows);
+          tx += b_rows[part] * 128;
+          if (PAIR) tx += mx4_box_rows(p.N, brow[part] + kRows, kRows) * 128;
+        }
+        auto map_b = [&](int part) -> const void* {
+          return b_rows[part] != L::part_rows(part) ? &maps.Bt : (part ? &maps.B1 : &maps.B);
+        };
         for (int kb = 0; kb < KB; ++kb) {
           if (!wait(empty_bar(stage), phase ^ 1u)) { ok = false; break; }
           const uint32_t at = stage_at(stage);
@@ -750,13 +779,17 @@ __global__ void __launch_bounds__(kMxThreads, 1)
           if (PAIR) {
             const uint32_t bar = map_to_cta(full_bar(stage), 0);
             if (a_rows) tma_load_2d_pair(at, map_a, kb * 128, m_blk * 128, bar, pol);
-            if (b_rows) tma_load_2d_pair(at + L::kABytes, map_b, kb * 128, brow, bar, pol_b);
+#pragma unroll
+            for (int part = 0; part < L::kParts; ++part)
+              if (b_rows[part])
+                tma_load_2d_pair(at + L::kABytes + part * L::kPartOffset, map_b(part), kb * 128, brow[part], bar, pol_b);
             tma_load_2d_pair(at + L::kSfaOffset, &maps.SA, kb * 256, m_blk, bar, pol);
             tma_load_2d_pair(at + L::kSfbOffset, &maps.SB, kb * 256, n_blk * BN >> 7, bar, pol_b);
           } else {
             const uint32_t bar = full_bar(stage);
             tma_load_2d(at, map_a, kb * 128, m_blk * 128, bar, pol);
-            tma_load_2d(at + L::kABytes, map_b, kb * 128, brow, bar, pol_b);
+            static_assert(PAIR || L::kParts == 1, "one CTA's B is one part");
+            tma_load_2d(at + L::kABytes, map_b(0), kb * 128, brow[0], bar, pol_b);
             tma_load_2d(at + L::kSfaOffset, &maps.SA, kb * 256, m_blk, bar, pol);
             tma_load_2d(at + L::kSfbOffset, &maps.SB, kb * 256, n_blk * BN >> 7, bar, pol_b);
           }
@@ -779,8 +812,8 @@ __global__ void __launch_bounds__(kMxThreads, 1)
       int local = 0;
       for (int tile = worker; tile < num_tiles && ok; tile += workers, ++local) {
         const int n_blk = tile % p.num_n_blocks;
-        const int acc = local & 1;
-        if (L::kOverlap) {  // the previous tile's shared columns have been drained
+        const int acc = L::kAccs == 1 ? 0 : local & 1;
+        if (L::kOverlap || L::kAccs == 1) {  // the columns that the previous tile held too have been drained
           if (local > 0 && !wait(tempty_bar(0), (local - 1) & 1u)) { ok = false; break; }
         } else {
           if (!wait(tempty_bar(acc), ((local >> 1) & 1u) ^ 1u)) { ok = false; break; }
@@ -816,10 +849,10 @@ __global__ void __launch_bounds__(kMxThreads, 1)
     int local = 0;
     for (int tile = worker; tile < num_tiles; tile += workers, ++local) {
       const int m_blk = (tile / p.num_n_blocks) * kRanks + static_cast<int>(rank), n_blk = tile % p.num_n_blocks;
-      const int acc = local & 1;
+      const int acc = L::kAccs == 1 ? 0 : local & 1;
       auto ready = [&] {
         bool got = false;
-        if (lane == 0) got = wait(tfull_bar(acc), (local >> 1) & 1u);
+        if (lane == 0) got = wait(tfull_bar(acc), (L::kAccs == 1 ? local : local >> 1) & 1u);
         if (!__shfl_sync(0xffffffffu, got, 0)) return false;
         tc_fence_after();
         return true;

@@ -2,10 +2,12 @@
 // (included by ngram_embed.cu after its own helpers).
 //
 // Kernels that follow one of their own (the product after the quantisation or the gather, the
-// lookup, the gradient's sums and join) are programmatic dependent launches: their set-up runs
-// while the kernel before ends, and they wait for all of it before their first global access.
-// In graphs: one token's projection 9.8 -> 9.1 us, a decode step's layer 24.3 -> 22.8, the
-// gradient of 32768 rows 111 -> 103.
+// lookup, the gradient's sums and join), and the quantisation, are programmatic dependent
+// launches: their set-up runs while the kernel before ends, and they wait for all of it before
+// their first global access. In graphs: one token's projection 9.8 -> 9.0 us, a decode step's
+// layer 24.3 -> 22.8, the gradient of 32768 rows 111 -> 103. The product, the lookup and the join
+// do not let their own dependents start early, nor is the cluster sort such a launch: the
+// projection of 1280 tokens took 17.5 us for 16.9, the gradient 118 for 97.
 #pragma once
 
 namespace {
@@ -117,18 +119,25 @@ struct Mx4Operands {
   const uint8_t *A, *SA, *B, *SB;  // codes and scale tiles
 };
 
-// The maps of a product whose tiles take 128 rows of A and b_rows of B a box (see Mx4Maps).
-int encode_mx4(Mx4Maps* m, const Mx4Operands& o, const Mx4GemmParams& p, int b_rows, int sfb_rows) {
+// The maps of a product on tiles of layout L (see Mx4Maps).
+template <typename L, int BN, int RANKS>
+int encode_mx4(Mx4Maps* m, const Mx4Operands& o, const Mx4GemmParams& p) {
   const int64_t kt = (p.K + 127) / 128;
   int rc;
   if ((rc = encode_codes(&m->A, o.A, p.K, p.M, 128))) return rc;
-  if ((rc = encode_codes(&m->B, o.B, p.K, p.N, b_rows))) return rc;
+  if ((rc = encode_codes(&m->B, o.B, p.K, p.N, L::part_rows(0)))) return rc;
+  m->B1 = m->B;
+  if (L::kParts > 1 && (rc = encode_codes(&m->B1, o.B, p.K, p.N, L::part_rows(1)))) return rc;
   m->At = m->A;
   m->Bt = m->B;
   if (p.M % 128 && (rc = encode_codes(&m->At, o.A, p.K, p.M, (p.M % 128 + 7) & ~7))) return rc;
-  if (p.N % b_rows && (rc = encode_codes(&m->Bt, o.B, p.K, p.N, (p.N % b_rows + 7) & ~7))) return rc;
+  for (int part = 0; part < L::kParts; ++part)  // the one box that N ends inside
+    for (int rank = 0; rank < RANKS; ++rank) {
+      const int rows = p.N % BN - L::part_row(part, rank);
+      if (rows > 0 && rows < L::part_rows(part) && (rc = encode_codes(&m->Bt, o.B, p.K, p.N, (rows + 7) & ~7))) return rc;
+    }
   if ((rc = encode_scales(&m->SA, o.SA, p.M, kt, 1))) return rc;
-  return encode_scales(&m->SB, o.SB, p.N, kt, sfb_rows);
+  return encode_scales(&m->SB, o.SB, p.N, kt, L::kSfbRows);
 }
 
 template <int BN, int STAGES, typename OutT, bool PAIR>
@@ -140,7 +149,7 @@ int launch_mx4_tiles(Mx4GemmParams prm, const Mx4Operands& o, int sms, cudaStrea
   Mx4Maps maps;
   int rc = opt_in_smem(kern, L::kLaunchBytes, done);
   if (rc) return rc;
-  if ((rc = encode_mx4(&maps, o, prm, PAIR ? BN / 2 : BN, L::kSfbRows))) return rc;
+  if ((rc = (encode_mx4<L, BN, PAIR ? 2 : 1>(&maps, o, prm)))) return rc;
   constexpr int kRows = PAIR ? 256 : 128;
   prm.num_m_blocks = (prm.M + kRows - 1) / kRows;
   prm.num_n_blocks = (prm.N + BN - 1) / BN;
@@ -153,21 +162,27 @@ int launch_mx4_tiles(Mx4GemmParams prm, const Mx4Operands& o, int sms, cudaStrea
                 prm);
 }
 
-// Which tiles: CTA pairs on 256 x 256 (the fewest bytes for their products), or one CTA on 128 x
-// 192, 128 or 64, whichever finishes its waves first by the times below: a wave of a form costs
-// so many us a k-block and so many besides, and never less than its epilogue. Measured on B200,
-// bf16 out (us, 256 / 192 / 128 / 64; * taken):
-//   32768 x 2048 x 2048   61.5* 72.4  82.9 150.4     1280 x 4096 x 4096  17.0  15.8* 18.5  27.2
-//    4096 x 4096 x 4096   28.7* 33.8  39.3  71.4     1280 x 2048 x 2048   8.6   6.6*  8.7  10.4
-//    8192 x 2048 x 2048   18.9* 19.6  22.9  39.7      512 x 4096 x 4096  11.0   9.2   8.4* 12.6
-//    5000 x 8192 x 320    30.2* 32.6  35.6  47.3      333 x 1111 x 2080  11.5  10.1   8.3   6.2*
-//   16384 x 1000 x 512    17.1  17.7  16.4* 19.5        1 x 4096 x 4096  10.0   8.4   7.6   7.2*
+// Which tiles: CTA pairs on 256 x 256 (the fewest bytes for their products) or 256 x 320 (fewer
+// tiles where those just exceed a wave, no overlap of a tile's epilogue with the next tile), or
+// one CTA on 128 x 192, 128 or 64, whichever finishes its waves first by the times below: a wave
+// of a form costs so many us a k-block and so many besides, and never less than its least.
+// Measured on B200, bf16 out (us, 320 / 256 / 192 / 128 / 64; * taken):
+//   32768 x 2048 x 2048   81.1  61.5* 72.4  82.9 150.4    1280 x 4096 x 4096  13.1* 17.0  16.0  18.8  27.2
+//    4096 x 4096 x 4096   30.9  28.7* 33.8  39.3  71.4    1280 x 2048 x 2048   9.6   8.6   6.6*  8.7  10.4
+//    8192 x 2048 x 2048   28.2  18.9* 19.6  22.9  39.7    1280 x 4096 x 1024   8.4  10.3   8.2*  8.8  10.4
+//     512 x 8192 x 4096   12.7  11.7* 15.6  14.5  22.5     512 x 4096 x 4096  12.4  11.0   9.2   8.4* 12.6
+//   37000 x  320 x 4096   24.6* 32.7  29.8  34.9  52.2   16384 x 1000 x  512     -  17.1  17.7  16.4* 19.5
+//     512 x 10000 x 4096  12.5* 16.2  16.0  18.6  26.9     333 x 1111 x 2080     -  11.5  10.1   8.3   6.2*
+//    9400 x  640 x 2048   10.0* 11.8  10.4  12.0  16.1       1 x 4096 x 4096     -  10.0   8.4   7.6   7.2*
 struct Mx4Form {
   int rows, cols;              // of a tile
   double us_kb, us_tile, least, once;  // a wave's us: for a k-block, besides, at least; the call's besides
 };
-constexpr Mx4Form kMx4Forms[4] = {
-    {256, 256, 0.32, 1.6, 3.1, 1.5}, {128, 192, 0.30, 1.3, 2.5, 0.0}, {128, 128, 0.26, 1.0, 1.75, 0.0}, {128, 64, 0.27, 0.5, 1.25, 0.0}};
+constexpr Mx4Form kMx4Forms[5] = {{256, 256, 0.32, 1.6, 3.1, 1.5},
+                                  {256, 320, 0.39, 3.2, 4.8, 0.3},
+                                  {128, 192, 0.30, 1.3, 2.5, 0.0},
+                                  {128, 128, 0.26, 1.0, 1.75, 0.0},
+                                  {128, 64, 0.27, 0.5, 1.25, 0.0}};
 int mx4_tile_width(int M, int N, int K, int sms) {
   int width = 0;
   double best = 0;
@@ -188,6 +203,7 @@ template <typename OutT>
 int launch_mx4_gemm(const Mx4GemmParams& prm, const Mx4Operands& o, int sms, cudaStream_t st) {
   if (sms < 2) return NGRAM_ERR_CUDA;
   switch (mx4_tile_width(prm.M, prm.N, prm.K, sms)) {
+    case 320: return launch_mx4_tiles<320, 5, OutT, true>(prm, o, sms, st);
     case 256: return launch_mx4_tiles<256, 5, OutT, true>(prm, o, sms, st);
     case 192: return launch_mx4_tiles<192, 5, OutT, false>(prm, o, sms, st);
     case 128: return launch_mx4_tiles<128, 6, OutT, false>(prm, o, sms, st);
@@ -483,9 +499,9 @@ int launch_quantize(Mx4QuantParams& p, uint32_t rows, uint32_t vecs, cudaStream_
   const int U = RowMap::unroll(vecs);
   p.map.set(rows, vecs, U);
   const dim3 grid = row_map_grid(p.map);
-  if (U == 4) return launch(mx4_quantize_kernel<T, VEC, 4>, grid, dim3(256), 0, st, false, 1, p);
-  if (U == 2) return launch(mx4_quantize_kernel<T, VEC, 2>, grid, dim3(256), 0, st, false, 1, p);
-  return launch(mx4_quantize_kernel<T, VEC, 1>, grid, dim3(256), 0, st, false, 1, p);
+  if (U == 4) return launch(mx4_quantize_kernel<T, VEC, 4>, grid, dim3(256), 0, st, true, 1, p);
+  if (U == 2) return launch(mx4_quantize_kernel<T, VEC, 2>, grid, dim3(256), 0, st, true, 1, p);
+  return launch(mx4_quantize_kernel<T, VEC, 1>, grid, dim3(256), 0, st, true, 1, p);
 }
 
 // Rows of a launch whose warps are numbered in 32 bits: at most 2^30 vectors of eight elements.

@@ -91,6 +91,7 @@ def test_quantising_what_a_quantised_row_stands_for_changes_nothing(ne):
     (33, 4096, 1024), (300, 1000, 2080), (640, 512, 4096), (1, 2048, 4096), (2000, 1536, 544),
     (600, 2048, 1056), (2300, 2048, 320), (2200, 2100, 96), (1290, 2047, 544), (700, 2500, 64), (3024, 5774, 64),
     (6864, 2528, 96), (2290, 2048, 1056), (2300, 2041, 2048),
+    (1279, 4095, 2080), (1100, 4352, 2304), (28600, 318, 1056),
 ])
 def test_product_within_the_bound_of_its_sums(ne, M, N, K, out_dtype):
     rng = np.random.default_rng(M * 7 + N * 3 + K)
@@ -107,7 +108,7 @@ def test_product_within_the_bound_of_its_sums(ne, M, N, K, out_dtype):
 def test_products_above_take_every_form_of_tiles(ne):
     sizes = [m.args[1] for m in test_product_within_the_bound_of_its_sums.pytestmark
              if m.name == "parametrize" and m.args[0] == "M,N,K"][0]
-    assert {ne.ngram_mx4_product_form(*s) for s in sizes} == {64, 128, 192, 256}
+    assert {ne.ngram_mx4_product_form(*s) for s in sizes} == {64, 128, 192, 256, 320}
 
 
 @pytest.mark.parametrize("out_dtype", [BF16, F32])
@@ -196,6 +197,7 @@ def test_layer_from_4bit_tables(ne, case, lengths):
 @pytest.mark.parametrize("dtype,D,N,K,lengths", [
     (BF16, 1024, 3, 1, [3000, 0, 1, 700, 299]), (F32, 1024, 3, 1, [3999]), (BF16, 1056, 4, 1, [2049, 2048]),
     (BF16, 1280, 5, 2, [1] * 3000), (BF16, 2048, 3, 2, [2300]), (F32, 2048, 3, 2, [1, 2299]), (BF16, 2080, 2, 1, [1200, 101]),
+    (BF16, 2240, 3, 1, [2500]), (F32, 2240, 3, 1, [1, 0, 2449]),
 ])
 def test_layer_of_many_tokens(ne, dtype, D, N, K, lengths):
     """Several tiles a CTA, in every form of them; twice on one workspace, then with ids out of
