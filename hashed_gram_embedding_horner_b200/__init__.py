@@ -635,7 +635,8 @@ def ngram_mx4_product(a: Mx4, b: Mx4, out, workspace, alpha: float = 1.0, stream
 
 
 def ngram_mx4_product_form(M: int, N: int, K: int, sms: int = 148) -> int:
-    """Columns of the tiles that a product takes on a device of `sms` SMs: 256 or 320 (CTA pairs), 192, 128 or 64."""
+    """Columns of the tiles that a product takes on a device of `sms` SMs: 256 or 320 (CTA pairs), 192,
+    128 or 64; 0 where up to four rows take a warp a column instead."""
     rc = _lib.ngram_mx4_product_form(int(M), int(N), int(K), int(sms))
     _check(min(rc, 0), "ngram_mx4_product_form")
     return rc

@@ -881,4 +881,133 @@ __global__ void __launch_bounds__(kMxThreads, 1)
   }
 }
 
+// ------------------------------------------------------------------ product of few rows
+//
+// The same product for at most R <= 4 rows of A, where a tile's 128 rows would be idle: a warp
+// takes one column n, its lanes the blocks of the row B[n], read once. Twice an E2M1 value is an
+// integer of magnitude at most 12, so a block's sum of 32 products is an exact integer by dp4a,
+// scaled by a power of two and added in fp32. A's rows are decoded to int8 in shared memory once
+// a block of eight warps. Bound by its instructions, about 60 a block of B and 12 more a row: one
+// token's 4096 x 4096 takes 4.6 us in a graph (7.2 on tiles), 8.9 MB that L2 holds; quantised
+// first and with B from HBM, 6.8 us (9.4). Asking L2 for B's rows before the wait for the
+// quantisation gained nothing.
+
+constexpr int kMxFewWarps = 8;
+constexpr int kMxFewUnroll = 4;                     // blocks of B in flight a lane
+constexpr int kMxFewBlocks = 32 * kMxFewUnroll;     // of a row, at a time
+
+struct Mx4FewParams {
+  Mx4GemmParams g;
+  const uint8_t *A, *SA, *B, *SB;  // codes and scale tiles
+};
+
+// Eight E2M1 codes to int8 of twice their values, in order. (Bytes of the magnitudes and of
+// their negatives by permutation, chosen by each code's sign spread over its byte.)
+__device__ __forceinline__ void e2m1x8_twice(uint32_t codes, uint32_t (&x)[2]) {
+  const uint32_t up = codes << 4;
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    const uint32_t sel = (codes >> (16 * h)) & 0x7777u;
+    uint32_t neg;  // the intrinsic has no sign mode
+    asm("prmt.b32 %0, %1, 0, 0xBA98;" : "=r"(neg) : "r"(__byte_perm(up, codes, h ? 0x7362 : 0x5140)));
+    const uint32_t pos_v = __byte_perm(0x03020100u, 0x0C080604u, sel), neg_v = __byte_perm(0xFDFEFF00u, 0xF4F8FAFCu, sel);
+    x[h] = (pos_v & ~neg) | (neg_v & neg);
+  }
+}
+
+// x * 2^e for a sum x of twice-values of two blocks with scale bytes ea and eb: 2^e in two
+// halves, which are normal where the result is not zero.
+__device__ __forceinline__ float mx4_scale_pair(int x, uint32_t ea, uint32_t eb) {
+  int e = static_cast<int>(ea + eb) - 256;  // 2 * 127, and twice two
+  e = max(e, -252);
+  const int h = e >> 1;
+  const float s1 = __uint_as_float(static_cast<uint32_t>(h + 127) << 23), s2 = __uint_as_float(static_cast<uint32_t>(e - h + 127) << 23);
+  const float v = static_cast<float>(x) * s1 * s2;
+  return ea == 255 || eb == 255 ? __uint_as_float(0x7FC00000u) : v;
+}
+
+template <int R, typename OutT>
+__global__ void __launch_bounds__(32 * kMxFewWarps) mx4_few_kernel(const __grid_constant__ Mx4FewParams p) {
+  __shared__ uint4 s_a[R][2][kMxFewBlocks];  // first and second halves of blocks: no bank conflicts
+  __shared__ uint8_t s_e[R][kMxFewBlocks];
+  pdl_wait();
+  const Mx4GemmParams& g = p.g;
+  const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
+  const int blocks = g.K / kMxBlock, kt = (g.K + 127) / 128;
+  // a block's columns share the 32-byte sectors of the scales' tiles: two neighbours in each quarter
+  const int n = (blockIdx.x >> 4) * 128 + (blockIdx.x & 15) * 2 + (w & 1) + (w >> 1) * 32;
+  const bool on = n < g.N;
+  const uint4* row = reinterpret_cast<const uint4*>(p.B) + static_cast<int64_t>(on ? n : 0) * blocks;
+  float acc[R];
+#pragma unroll
+  for (int r = 0; r < R; ++r) acc[r] = 0.f;
+  for (int b0 = 0; b0 < blocks; b0 += kMxFewBlocks) {
+    uint4 code[kMxFewUnroll];
+    uint32_t eb[kMxFewUnroll];
+#pragma unroll
+    for (int u = 0; u < kMxFewUnroll; ++u) {
+      const int b = b0 + u * 32 + lane;
+      code[u] = make_uint4(0, 0, 0, 0);
+      eb[u] = 0;
+      if (on && b < blocks) {
+        code[u] = ld_stream_v4(row + b);
+        eb[u] = __ldg(p.SB + mx4_tile_at(n, b, kt));
+      }
+    }
+    if (b0) __syncthreads();
+    for (int i = threadIdx.x; i < R * kMxFewBlocks; i += 32 * kMxFewWarps) {
+      const int r = i / kMxFewBlocks, k = i % kMxFewBlocks, b = b0 + k;
+      uint4 c = make_uint4(0, 0, 0, 0);
+      uint32_t e = 0;
+      if (r < g.M && b < blocks) {
+        c = __ldg(reinterpret_cast<const uint4*>(p.A) + static_cast<int64_t>(r) * blocks + b);
+        e = __ldg(p.SA + mx4_tile_at(r, b, kt));
+      }
+      uint32_t x[4][2];
+      e2m1x8_twice(c.x, x[0]);
+      e2m1x8_twice(c.y, x[1]);
+      e2m1x8_twice(c.z, x[2]);
+      e2m1x8_twice(c.w, x[3]);
+      s_a[r][0][k] = make_uint4(x[0][0], x[0][1], x[1][0], x[1][1]);
+      s_a[r][1][k] = make_uint4(x[2][0], x[2][1], x[3][0], x[3][1]);
+      s_e[r][k] = static_cast<uint8_t>(e);
+    }
+    __syncthreads();
+#pragma unroll
+    for (int u = 0; u < kMxFewUnroll; ++u) {
+      const int k = u * 32 + lane;
+      if (b0 + u * 32 >= blocks) break;
+      uint32_t y[4][2];
+      e2m1x8_twice(code[u].x, y[0]);
+      e2m1x8_twice(code[u].y, y[1]);
+      e2m1x8_twice(code[u].z, y[2]);
+      e2m1x8_twice(code[u].w, y[3]);
+#pragma unroll
+      for (int r = 0; r < R; ++r) {
+        const uint4 lo = s_a[r][0][k], hi = s_a[r][1][k];
+        const uint32_t x[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
+        int d = 0;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) d = __dp4a(static_cast<int>(x[j]), static_cast<int>(y[j >> 1][j & 1]), d);
+        acc[r] += mx4_scale_pair(d, s_e[r][k], eb[u]);
+      }
+    }
+  }
+  float mine = 0.f;
+#pragma unroll
+  for (int r = 0; r < R; ++r) {
+    float v = acc[r];
+#pragma unroll
+    for (int o = 16; o; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+    if (lane == r) mine = v;
+  }
+  if (!on || lane >= R || lane >= g.M) return;
+  const OutT* e0 = mx4_e0_row<OutT>(g, lane);
+  OutT* out = static_cast<OutT*>(g.out) + static_cast<int64_t>(lane) * g.ldo + n;
+  if constexpr (sizeof(OutT) == 2)
+    *out = static_cast<uint16_t>(pack_bf16x2((mine + (e0 ? bf16_bits_to_float(e0[n]) : 0.f)) * g.scale, 0.f));
+  else
+    *out = (mine + (e0 ? e0[n] : 0.f)) * g.scale;
+}
+
 }  // namespace ngram

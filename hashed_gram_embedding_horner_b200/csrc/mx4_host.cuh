@@ -183,15 +183,30 @@ constexpr Mx4Form kMx4Forms[5] = {{256, 256, 0.32, 1.6, 3.1, 1.5},
                                   {128, 192, 0.30, 1.3, 2.5, 0.0},
                                   {128, 128, 0.26, 1.0, 1.75, 0.0},
                                   {128, 64, 0.27, 0.5, 1.25, 0.0}};
+// 0: no tiles, a warp a column (mx4_few_kernel), for up to four rows where that is sooner: it costs
+// an element of B so much a row and in any case, all of B on this many SMs, and a tile form about
+// 1.7 us more than it before the first wave. 1 / 4 rows, us (tiles in brackets): 4096 x 4096
+// 4.6 / 6.8 (7.2), 2048 x 2048 2.3 / 3.4 (4.9), 512 x 512 1.6 / 2.4 (3.1), 16384 x 16384 43 / 74
+// (40); rows of B much shorter than the 4096 elements that a warp takes at a time leave lanes
+// idle: 50000 x 1024 19 / 33 (12).
+constexpr int kMx4FewRows = 4;
+double mx4_few_us(int M, int N, int K, int sms) {
+  const double elements = static_cast<double>(N) * ((K + 4095) / 4096) * 4096;
+  return elements * (0.13 + 0.04 * M) * 1e-6 * 148 / sms - 1.7;
+}
 int mx4_tile_width(int M, int N, int K, int sms) {
-  int width = 0;
+  int width = -1;
   double best = 0;
+  if (M <= kMx4FewRows) {
+    width = 0;
+    best = mx4_few_us(M, N, K, sms);
+  }
   for (const Mx4Form& f : kMx4Forms) {
     const int64_t tiles = (static_cast<int64_t>(M) + f.rows - 1) / f.rows * ((static_cast<int64_t>(N) + f.cols - 1) / f.cols);
     const int64_t workers = sms * 128 / f.rows, waves = (tiles + workers - 1) / workers;
     const double wave = (K + 255) / 256 * f.us_kb + f.us_tile;
     const double us = f.once + static_cast<double>(waves) * (wave > f.least ? wave : f.least);
-    if (!width || us < best) {
+    if (width < 0 || us < best) {
       width = f.cols;
       best = us;
     }
@@ -199,10 +214,21 @@ int mx4_tile_width(int M, int N, int K, int sms) {
   return width;
 }
 
+template <int R, typename OutT>
+int launch_mx4_few(const Mx4GemmParams& prm, const Mx4Operands& o, cudaStream_t st) {
+  const Mx4FewParams p{prm, o.A, o.SA, o.B, o.SB};
+  return launch(mx4_few_kernel<R, OutT>, dim3(static_cast<unsigned>((prm.N + 127) / 128 * 16)), dim3(32 * kMxFewWarps), 0, st,
+                true, 1, p);
+}
+
 template <typename OutT>
 int launch_mx4_gemm(const Mx4GemmParams& prm, const Mx4Operands& o, int sms, cudaStream_t st) {
   if (sms < 2) return NGRAM_ERR_CUDA;
-  switch (mx4_tile_width(prm.M, prm.N, prm.K, sms)) {
+  const int width = mx4_tile_width(prm.M, prm.N, prm.K, sms);
+  if (width == 0)
+    return prm.M == 1 ? launch_mx4_few<1, OutT>(prm, o, st)
+                      : (prm.M == 2 ? launch_mx4_few<2, OutT>(prm, o, st) : launch_mx4_few<4, OutT>(prm, o, st));
+  switch (width) {
     case 320: return launch_mx4_tiles<320, 5, OutT, true>(prm, o, sms, st);
     case 256: return launch_mx4_tiles<256, 5, OutT, true>(prm, o, sms, st);
     case 192: return launch_mx4_tiles<192, 5, OutT, false>(prm, o, sms, st);

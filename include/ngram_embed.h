@@ -370,7 +370,8 @@ int ngram_mx4_product(const ngram_mx4* A, const ngram_mx4* B, int64_t M, int64_t
 
 /* The tiles that a product of these sizes takes on a device of `sms` SMs (the layer on 4-bit
  * tables: M tokens, N = K = D, the plan's SM count): 256 or 320 = CTA pairs on 256 rows x that many
- * columns; 192, 128 or 64 = one CTA on 128 rows. Negative on bad arguments. */
+ * columns; 192, 128 or 64 = one CTA on 128 rows; 0 = no tiles, a warp a column (at most four
+ * rows). Negative on bad arguments. */
 int ngram_mx4_product_form(int64_t M, int64_t N, int64_t K, int sms);
 
 /* The whole layer (Eq. 2 + Eq. 3) with 4-bit sub-tables and a 4-bit projection:

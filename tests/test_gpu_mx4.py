@@ -92,6 +92,7 @@ def test_quantising_what_a_quantised_row_stands_for_changes_nothing(ne):
     (600, 2048, 1056), (2300, 2048, 320), (2200, 2100, 96), (1290, 2047, 544), (700, 2500, 64), (3024, 5774, 64),
     (6864, 2528, 96), (2290, 2048, 1056), (2300, 2041, 2048),
     (1279, 4095, 2080), (1100, 4352, 2304), (28600, 318, 1056),
+    (1, 4096, 4096), (2, 2041, 64), (3, 1000, 4128), (4, 130, 8224), (2, 129, 4096), (4, 512, 512),
 ])
 def test_product_within_the_bound_of_its_sums(ne, M, N, K, out_dtype):
     rng = np.random.default_rng(M * 7 + N * 3 + K)
@@ -108,40 +109,42 @@ def test_product_within_the_bound_of_its_sums(ne, M, N, K, out_dtype):
 def test_products_above_take_every_form_of_tiles(ne):
     sizes = [m.args[1] for m in test_product_within_the_bound_of_its_sums.pytestmark
              if m.name == "parametrize" and m.args[0] == "M,N,K"][0]
-    assert {ne.ngram_mx4_product_form(*s) for s in sizes} == {64, 128, 192, 256, 320}
+    assert {ne.ngram_mx4_product_form(*s) for s in sizes} == {0, 64, 128, 192, 256, 320}
 
 
+@pytest.mark.parametrize("rows", [37, 3])
 @pytest.mark.parametrize("out_dtype", [BF16, F32])
-def test_product_writes_only_its_own_columns(ne, out_dtype):
+def test_product_writes_only_its_own_columns(ne, out_dtype, rows):
     rng = np.random.default_rng(3)
-    a, b = ref.random_mx4(rng, 37, 96), ref.random_mx4(rng, 41, 96)
+    a, b = ref.random_mx4(rng, rows, 96), ref.random_mx4(rng, 41, 96)
     av, bv = ref.values(*a), ref.values(*b)
     want = av @ bv.T
     for lo, width in ((0, 64), (3, 57), (8, 72)):
-        buf = torch.full((39, width), 7.0, dtype=out_dtype, device="cuda")
-        out = buf[1:38, lo:lo + 41]
+        buf = torch.full((rows + 2, width), 7.0, dtype=out_dtype, device="cuda")
+        out = buf[1:rows + 1, lo:lo + 41]
         ne.ngram_mx4_product(device_mx4(ne, *a, ne.MX4_TILES), device_mx4(ne, *b, ne.MX4_TILES), out,
-                             ne.new_mx4_workspace(37, 41, 96))
+                             ne.new_mx4_workspace(rows, 41, 96))
         assert (np.abs(f64(out) - want) <= ref.product_bound(av, bv, HALF[out_dtype], want)).all()
         out.fill_(7.0)
         assert bool((buf == 7.0).all())
 
 
-def test_product_carries_nan_blocks_and_wide_scales(ne):
+@pytest.mark.parametrize("rows", [130, 4, 1])
+def test_product_carries_nan_blocks_and_wide_scales(ne, rows):
     """A NaN block makes its row (of A) or column (of B) NaN and nothing else; scales at the
     ends of the range multiply as powers of two."""
     rng = np.random.default_rng(9)
-    a, b = ref.random_mx4(rng, 130, 256), ref.random_mx4(rng, 70, 256)
-    a[1][129, 3] = 255
+    a, b = ref.random_mx4(rng, rows, 256), ref.random_mx4(rng, 70, 256)
+    a[1][rows - 1, 3] = 255
     b[1][5, 0] = 255
-    out = torch.empty((130, 70), device="cuda")
-    ws = ne.new_mx4_workspace(130, 70, 256)
+    out = torch.empty((rows, 70), device="cuda")
+    ws = ne.new_mx4_workspace(rows, 70, 256)
     ne.ngram_mx4_product(device_mx4(ne, *a, ne.MX4_TILES), device_mx4(ne, *b, ne.MX4_TILES), out, ws)
     av, bv = ref.values(*a), ref.values(*b)
     got, want = f64(out), av @ bv.T
-    assert np.isnan(got[129]).all() and np.isnan(got[:, 5]).all()
+    assert np.isnan(got[rows - 1]).all() and np.isnan(got[:, 5]).all()
     ok = ~np.isnan(want)
-    assert ok.sum() == 129 * 69
+    assert ok.sum() == (rows - 1) * 69
     assert (np.abs(got - want)[ok] <= ref.product_bound(np.nan_to_num(av), np.nan_to_num(bv), ref.F32_HALF,
                                                         np.nan_to_num(want))[ok]).all()
     a[1][:], b[1][:] = 0, 254  # 2^-127 and 2^127: the product's scales cancel
@@ -176,7 +179,7 @@ LAYERS = [  # V0, D, N, K, V, dtype
 ]
 
 
-@pytest.mark.parametrize("lengths", [[1], [5, 0, 1, 3], [127, 2], [100, 300, 0, 41], [1300]])
+@pytest.mark.parametrize("lengths", [[1], [1, 2], [5, 0, 1, 3], [127, 2], [100, 300, 0, 41], [1300]])
 @pytest.mark.parametrize("case", range(len(LAYERS)))
 def test_layer_from_4bit_tables(ne, case, lengths):
     V0, D, N, K, V, dtype = LAYERS[case]
@@ -387,7 +390,7 @@ def test_products_of_every_form_at_once_on_two_streams(ne):
     workspaces: each result has the bits of its call alone."""
     rng = np.random.default_rng(41)
     calls = []
-    for M, N, K in ((2000, 1536, 256), (1280, 1024, 256), (700, 520, 320), (1, 640, 96)):
+    for M, N, K in ((2000, 1536, 256), (1280, 1024, 256), (700, 520, 320), (20, 640, 96), (1, 640, 4128)):
         a, b = (device_mx4(ne, *ref.random_mx4(rng, r, K), ne.MX4_TILES) for r in (M, N))
         out, ws = torch.empty((M, N), dtype=BF16, device="cuda"), ne.new_mx4_workspace(M, N, K)
         ne.ngram_mx4_product(a, b, out, ws)

@@ -72,7 +72,7 @@ def test_product_refusals(ne):
 @pytest.mark.parametrize("M,N,K,sms,form", [
     (32768, 2048, 2048, 148, 256), (65536, 4096, 4096, 148, 256), (2300, 2048, 2048, 148, 256),  # 72 of 74 pairs' tiles
     (1280, 4096, 4096, 148, 320), (1280, 4096, 1024, 148, 192), (28600, 318, 1056, 148, 320), (1280, 2048, 2048, 148, 192), (512, 4096, 4096, 148, 128), (333, 1111, 2080, 148, 64),
-    (1, 4096, 4096, 148, 64), (1, 1, 32, 2, 64), (1280, 4096, 4096, 40, 256),
+    (5, 4096, 4096, 148, 64), (4, 4096, 4096, 148, 0), (1, 16384, 16384, 148, 128), (1, 1, 32, 2, 0), (5, 1, 32, 2, 64), (1280, 4096, 4096, 40, 256),
 ])
 def test_product_tiles_for_a_device_size(ne, M, N, K, sms, form):
     assert ne.ngram_mx4_product_form(M, N, K, sms) == form
