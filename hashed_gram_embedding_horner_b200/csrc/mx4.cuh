@@ -887,9 +887,10 @@ __global__ void __launch_bounds__(kMxThreads, 1)
 // takes one column n, its lanes the blocks of the row B[n], read once. Twice an E2M1 value is an
 // integer of magnitude at most 12, so a block's sum of 32 products is an exact integer by dp4a,
 // scaled by a power of two and added in fp32. A's rows are decoded to int8 in shared memory once
-// a block of eight warps. Bound by its instructions, about 60 a block of B and 12 more a row: one
-// token's 4096 x 4096 takes 4.6 us in a graph (7.2 on tiles), 8.9 MB that L2 holds; quantised
-// first and with B from HBM, 6.8 us (9.4). Asking L2 for B's rows before the wait for the
+// a block of eight warps. One token's 4096 x 4096 takes 4.6 us in a graph (7.2 on tiles), 8.9 MB
+// that L2 holds, and 6.8 (9.4) with B from HBM and the quantisation in front: the launch and one
+// round of loads, an instruction a clock. Large products are bound by its instructions, about 60
+// a block of B and 12 more a row. Asking L2 for B's rows before the wait for the
 // quantisation gained nothing.
 
 constexpr int kMxFewWarps = 8;
