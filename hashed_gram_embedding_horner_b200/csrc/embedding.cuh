@@ -679,6 +679,7 @@ __global__ void __launch_bounds__(kClusterThreads, 1) sort_cluster_kernel(const 
   constexpr int kWarpItems = 32 * ITEMS;
   extern __shared__ __align__(16) uint8_t cluster_raw[];
   auto& m = *reinterpret_cast<ClusterSmem<ITEMS>*>(cluster_raw);
+  pdl_wait();
   pdl_launch_dependents();
   const SortParams& p = a.s;
   const int tid = threadIdx.x, lane = tid & 31, w = tid >> 5;

@@ -1,13 +1,13 @@
 // Host side of the 4-bit table operators and of the table lookup with its gradient
 // (included by ngram_embed.cu after its own helpers).
 //
-// Kernels that follow one of their own (the product after the quantisation or the gather, the
-// lookup, the gradient's sums and join), and the quantisation, are programmatic dependent
-// launches: their set-up runs while the kernel before ends, and they wait for all of it before
-// their first global access. In graphs: one token's projection 9.8 -> 9.0 us, a decode step's
-// layer 24.3 -> 22.8, the gradient of 32768 rows 111 -> 103. The product, the lookup and the join
-// do not let their own dependents start early, nor is the cluster sort such a launch: the
-// projection of 1280 tokens took 17.5 us for 16.9, the gradient 118 for 97.
+// All but the tiled sort are programmatic dependent launches: a kernel's set-up runs while the one
+// before ends, and it waits for all of that before its first global access. In graphs: one
+// token's projection 9.8 -> 9.0 us, a decode step's layer 24.3 -> 22.8, the gradient of 32768 rows
+// 111 -> 103; one call after another, for the first kernels of the calls: the step's layer
+// 24.4 -> 22.1, the gradients of 32768 and 641 rows 101.3 -> 99.1, 18.7 -> 16.9. The product, the
+// lookup and the join do not let their own dependents start early: the projection of 1280 tokens
+// took 17.5 us for 16.9, the gradient 118 for 97.
 #pragma once
 
 namespace {
@@ -295,7 +295,7 @@ int project_mx4(const ngram_embed_plan* p, const HashParams& h, const int32_t* i
   if (tokens > kMx4GatherMaxTokens) tokens = kMx4GatherMaxTokens;
   g.tokens = tokens < 8 ? 8 : tokens;
   int rc = launch(mx4_gather_kernel, dim3(static_cast<unsigned>((T + g.tokens - 1) / g.tokens)), dim3(kMx4GatherThreads), 0,
-                  st, p->pdl, 1, g);
+                  st, true, 1, g);
   if (rc) return rc;
   Mx4GemmParams prm{};
   prm.M = static_cast<int>(T);
@@ -396,7 +396,7 @@ int launch_cluster_sort(const ClusterSortParams& a, int64_t n, cudaStream_t st) 
   if (rc) return rc;
   int ctas = 1;
   while (static_cast<int64_t>(ctas) * kClusterThreads * ITEMS < n) ctas *= 2;
-  return launch(sort_cluster_kernel<ITEMS>, dim3(static_cast<unsigned>(ctas)), dim3(kClusterThreads), bytes, st, false, ctas,
+  return launch(sort_cluster_kernel<ITEMS>, dim3(static_cast<unsigned>(ctas)), dim3(kClusterThreads), bytes, st, true, ctas,
                 a);
 }
 

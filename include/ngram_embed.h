@@ -600,7 +600,8 @@ int ngram_embed_plan_set_stream_k(ngram_embed_plan* plan, int mode);
  * (barriers, tensor-memory allocation) until that kernel has completed and its writes are
  * visible. 0 (default) = plain launches: measured on B200 inside CUDA graphs, the gap
  * between launches is already about 1 us, and early-scheduled grids slowed the decode
- * step's hash -> projection pair down. Results do not change. */
+ * step's hash -> projection pair down. Results do not change. The calls on 4-bit tables and a
+ * table's lookup and gradient always launch so. */
 int ngram_embed_plan_set_pdl(ngram_embed_plan* plan, int on);
 
 #ifdef __cplusplus
