@@ -704,8 +704,8 @@ def new_embedding_workspace(max_ids: int, D: int, device="cuda"):
 
 
 def ngram_embedding_fwd(table, ids, out, workspace, scale: float = 1.0, pad_id: int = -1, stream=None):
-    """out[i] = scale * table[ids[i]]; ids None: the table's first rows in order. The table is a
-    contiguous bf16 or f32 matrix, or an Mx4 by rows; positions of pad_id get zeros."""
+    """out[i] = scale * table[ids[i]]; ids None: 0, 1, .. (the table's first rows in order). The
+    table is a contiguous bf16 or f32 matrix, or an Mx4 by rows; positions of pad_id get zeros."""
     out_code, n, D, stride = _matrix(out, "out")
     dev = out.get_device()
     if type(table) is Mx4:

@@ -34,6 +34,7 @@ struct LookupParams {
   void* out;              // of position 0 of this launch, row stride out_stride elements
   int64_t out_stride;
   int64_t row0;           // first row of this launch when ids is nullptr
+  uint32_t pad_pos;       // position of this launch whose row is pad_id then (2^32 - 1: none)
   int* status;
 };
 
@@ -88,7 +89,7 @@ __global__ void __launch_bounds__(256) lookup_kernel(const __grid_constant__ Loo
   for (int r = 0; r < R; ++r) {
     const uint32_t pos = part.row0 + r * part.row_step;
     int64_t row = p.row0 + pos;
-    zero[r] = pos >= p.map.rows;
+    zero[r] = pos >= p.map.rows || pos == p.pad_pos;
     if (p.ids && !zero[r]) {
       const int32_t id = __ldg(p.ids + pos);
       zero[r] = p.pad_id >= 0 && id == p.pad_id;

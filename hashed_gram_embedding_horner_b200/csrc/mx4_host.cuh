@@ -705,6 +705,7 @@ int ngram_embedding_fwd(const void* table, const void* table_scales, int table_d
     p.out = static_cast<uint8_t*>(out) + r0 * out_stride * elt;
     p.out_stride = out_stride;
     p.row0 = r0;
+    p.pad_pos = !ids && pad_id >= r0 && pad_id - r0 < r ? static_cast<uint32_t>(pad_id - r0) : UINT32_MAX;
     p.status = status_ptr(workspace);
     const cudaStream_t st = static_cast<cudaStream_t>(stream);
     int rc;

@@ -313,3 +313,24 @@ def test_padding_at_the_table_s_edges(ne, pad_id):
     np.add.at(want, row[~pad], g[~pad].astype(np.float64))
     assert np.array_equal(f64(out), np.where(pad[:, None], 0.0, table[row]))
     assert np.array_equal(f64(d), want)  # sums of at most 600 integers below 17: exact
+
+
+@pytest.mark.parametrize("kind", ["bf16", "f32", "mx4"])
+def test_whole_table_is_the_lookup_of_its_rows_in_order(ne, kind):
+    """ids None stands for 0, 1, ..: the same bits as those ids given, padding included."""
+    rng = np.random.default_rng(61)
+    V, D, n = 90, 96, 83
+    if kind == "mx4":
+        codes, scales = ref.random_mx4(rng, V, D)
+        table = ne.Mx4(torch.from_numpy(ref.pack(codes)).cuda(), torch.from_numpy(scales).cuda(), V, D, ne.MX4_ROWS)
+    else:
+        table = torch.from_numpy(rng.standard_normal((V, D)) + 10).to(BF16 if kind == "bf16" else F32).cuda()
+    ws = ne.new_embedding_workspace(0, D)
+    ids = torch.arange(n, dtype=torch.int32, device="cuda")
+    for pad in (-1, 0, 3, n - 1, n, V - 1, V, 1 << 31, (1 << 32) + 3):
+        got, want = (torch.full((n, D), 9.0, device="cuda") for _ in range(2))
+        ne.ngram_embedding_fwd(table, None, got, ws, scale=0.7, pad_id=pad)
+        ne.ngram_embedding_fwd(table, ids, want, ws, scale=0.7, pad_id=pad)
+        assert torch.equal(got, want)
+        assert bool((got[pad] == 0).all()) if 0 <= pad < n else bool((got != 0).any(dim=1).all())
+    assert ne.ngram_embed_get_status(ws) == 0
