@@ -147,10 +147,12 @@ __global__ void __launch_bounds__(256) lookup_kernel(const __grid_constant__ Loo
 #pragma unroll
             for (int j = 0; j < 8; ++j) x[j] *= f;
           } else {
-            // 2^k in two halves around the scale: each product by one is exact, so a value is
-            // rounded once, at the scale, and overflows only if the result does
+            // a scale, a power of two or results near fp32's ends: the product is exact in 64 bits
+            // (24 + 2 bits, exponents of at most 300), so it is rounded once, and overflows or
+            // vanishes only if the result does
+            const double w = static_cast<double>(s1) * static_cast<double>(p.scale) * static_cast<double>(s2);
 #pragma unroll
-            for (int j = 0; j < 8; ++j) x[j] = x[j] * s1 * p.scale * s2;
+            for (int j = 0; j < 8; ++j) x[j] = static_cast<float>(static_cast<double>(x[j]) * w);
           }
         }
       }

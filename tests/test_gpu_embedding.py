@@ -334,3 +334,21 @@ def test_whole_table_is_the_lookup_of_its_rows_in_order(ne, kind):
         assert torch.equal(got, want)
         assert bool((got[pad] == 0).all()) if 0 <= pad < n else bool((got != 0).any(dim=1).all())
     assert ne.ngram_embed_get_status(ws) == 0
+
+
+@pytest.mark.parametrize("scale", [3e38, -3.4e38, 2.0 ** 127, 1.5, 0.37, 2.0 ** -126, 1.1754942e-38, 1.37 * 2.0 ** -140,
+                                   -2.0 ** -149, 0.0])
+def test_lookup_of_every_4bit_value_rounds_its_product_once(ne, scale):
+    """All codes under all scale bytes times scales up to fp32's ends: the fp32 number nearest
+    to the product, then the bf16 number nearest to that. A product of a 24-bit scale, a code
+    of two bits and a power of two is exact in 64 bits."""
+    codes = np.tile(np.arange(16, dtype=np.uint8), (256, 2))
+    scales = np.arange(256, dtype=np.uint8)[:, None]
+    table = ne.Mx4(torch.from_numpy(ref.pack(codes)).cuda(), torch.from_numpy(scales).cuda(), 256, 32, ne.MX4_ROWS)
+    with np.errstate(over="ignore", under="ignore", invalid="ignore"):
+        want = torch.from_numpy((ref.values(codes, scales) * np.float64(np.float32(scale))).astype(np.float32))
+    ws = ne.new_embedding_workspace(0, 32)
+    for dtype in (F32, BF16):
+        out = torch.full((256, 32), 9.0, dtype=dtype, device="cuda")
+        ne.ngram_embedding_fwd(table, None, out, ws, scale=scale)
+        assert torch.allclose(out.cpu(), want.to(dtype), rtol=0, atol=0, equal_nan=True)
