@@ -55,6 +55,7 @@ EXPORTED = [
     "ngram_mx4_product_form",
     "ngram_embed_mx4_workspace_bytes", "ngram_embed_fwd_mx4", "ngram_embed_project_mx4",
     "ngram_embedding_workspace_bytes", "ngram_embedding_fwd", "ngram_embedding_bwd", "ngram_embedding_bwd_rows",
+    "ngram_embedding_sort_ctas",
 ]
 
 
@@ -133,6 +134,7 @@ _sig("ngram_embed_mx4_workspace_bytes", [_P, _I64], _SZ)
 _sig("ngram_embed_fwd_mx4", [_P, _P, _P, _I32, _I64, _P, _MX, _MX, _P, _P, _P, _P, _SZ, _P])
 _sig("ngram_embed_project_mx4", [_P, _P, _P, _I64, _P, _MX, _MX, _P, _P, _SZ, _P])
 _sig("ngram_embedding_workspace_bytes", [_I64, _I64], _SZ)
+_sig("ngram_embedding_sort_ctas", [_I64, ctypes.c_int])
 _sig("ngram_embedding_fwd", [_P, _P, ctypes.c_int, _I64, _I64, _P, _I64, ctypes.c_float, _I64, _P, ctypes.c_int, _I64,
                              _P, _SZ, _P])
 _sig("ngram_embedding_bwd", [_P, _I64, _P, ctypes.c_int, _I64, _I64, _I64, ctypes.c_float, _I64, _P, _P, _SZ, _P])
@@ -725,6 +727,14 @@ def ngram_embedding_fwd(table, ids, out, workspace, scale: float = 1.0, pad_id: 
                                   pad_id, out.data_ptr(), out_code, stride, ws, ws_bytes, _stream_of(stream, dev))
     if rc:
         _check(rc, "ngram_embedding_fwd")
+
+
+def ngram_embedding_sort_ctas(n: int, limit: int = 16) -> int:
+    """CTAs of the cluster that sorts a gradient's n ids on a device that places clusters of up to
+    `limit` CTAs; 0 where they are sorted in tiles."""
+    rc = _lib.ngram_embedding_sort_ctas(int(n), int(limit))
+    _check(min(rc, 0), "ngram_embedding_sort_ctas")
+    return rc
 
 
 def _f32_dense(t, name, device):

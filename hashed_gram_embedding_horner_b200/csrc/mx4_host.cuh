@@ -388,16 +388,64 @@ GradWs grad_ws(int64_t n, int64_t D, void* ws) {
   return w;
 }
 
+// The cluster that sorts n positions: `ctas` of them with `items` positions a thread, the fewest
+// items first, of at most `limit` CTAs. {0, 0}: it holds too few, they are sorted in tiles.
+struct ClusterForm {
+  int items, ctas;
+};
+ClusterForm cluster_form(int64_t n, int limit) {
+  for (int items = 1; items <= kClusterMaxItems; items *= 2) {
+    int ctas = 1;
+    while (ctas < limit && static_cast<int64_t>(ctas) * kClusterThreads * items < n) ctas *= 2;
+    if (ctas <= limit && static_cast<int64_t>(ctas) * kClusterThreads * items >= n) return {items, ctas};
+  }
+  return {0, 0};
+}
+
 template <int ITEMS>
-int launch_cluster_sort(const ClusterSortParams& a, int64_t n, cudaStream_t st) {
+int opt_in_cluster_sort() {
   static std::atomic<uint64_t> done{0};
-  constexpr int bytes = sizeof(ClusterSmem<ITEMS>);
-  const int rc = opt_in_smem(sort_cluster_kernel<ITEMS>, bytes, done, true);
+  return opt_in_smem(sort_cluster_kernel<ITEMS>, sizeof(ClusterSmem<ITEMS>), done, true);
+}
+
+// The most CTAs, up to kClusterCtas, of a cluster of the sort that the current device places:
+// fewer than 16 on a part of a GPU whose SM groups are smaller, 0 for none. Asked once a device,
+// for the form that takes the most shared memory. Negative on an error.
+int cluster_limit() {
+  static std::atomic<int> known[64];  // 1 + the answer
+  int dev = -1;
+  if (cudaGetDevice(&dev) != cudaSuccess) return NGRAM_ERR_CUDA;
+  if (dev < 64)
+    if (const int k = known[dev].load(std::memory_order_acquire)) return k - 1;
+  if (opt_in_cluster_sort<kClusterMaxItems>()) return NGRAM_ERR_CUDA;
+  int limit = 0;
+  for (int ctas = kClusterCtas; ctas && !limit; ctas /= 2) {
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = static_cast<unsigned>(ctas);
+    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(static_cast<unsigned>(ctas));
+    cfg.blockDim = dim3(kClusterThreads);
+    cfg.dynamicSmemBytes = sizeof(ClusterSmem<kClusterMaxItems>);
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    int fit = 0;
+    if (cudaOccupancyMaxActiveClusters(&fit, sort_cluster_kernel<kClusterMaxItems>, &cfg) != cudaSuccess)
+      (void)cudaGetLastError();  // a size that the device does not know
+    else if (fit > 0)
+      limit = ctas;
+  }
+  if (dev < 64) known[dev].store(limit + 1, std::memory_order_release);
+  return limit;
+}
+
+template <int ITEMS>
+int launch_cluster_sort(const ClusterSortParams& a, int ctas, cudaStream_t st) {
+  const int rc = opt_in_cluster_sort<ITEMS>();
   if (rc) return rc;
-  int ctas = 1;
-  while (static_cast<int64_t>(ctas) * kClusterThreads * ITEMS < n) ctas *= 2;
-  return launch(sort_cluster_kernel<ITEMS>, dim3(static_cast<unsigned>(ctas)), dim3(kClusterThreads), bytes, st, true, ctas,
-                a);
+  return launch(sort_cluster_kernel<ITEMS>, dim3(static_cast<unsigned>(ctas)), dim3(kClusterThreads),
+                sizeof(ClusterSmem<ITEMS>), st, true, ctas, a);
 }
 
 template <typename T>
@@ -430,7 +478,10 @@ int embedding_bwd(const int32_t* ids, int64_t n, const void* g, int g_dtype, int
   // keys 0 .. V (V: a padded position) in equal digits
   int bits = 1;
   while ((V >> bits) != 0) ++bits;
-  const bool cluster = n <= kClusterMax;
+  const int limit = n <= kClusterMax ? cluster_limit() : 0;
+  if (limit < 0) return limit;
+  const ClusterForm form = cluster_form(n, limit);
+  const bool cluster = form.ctas > 0;
   const int max_bits = cluster ? kClusterMaxBits : kSortMaxBits;
   const int passes = (bits + max_bits - 1) / max_bits;
   SortParams s{};
@@ -470,9 +521,8 @@ int embedding_bwd(const int32_t* ids, int64_t n, const void* g, int g_dtype, int
     r.key = w.key[0];
     r.pos = w.pos[0];
     const ClusterSortParams a{s, passes, r};
-    const int64_t per = int64_t(kClusterThreads) * kClusterCtas;
-    rc = n <= per ? launch_cluster_sort<1>(a, n, st) : (n <= 2 * per ? launch_cluster_sort<2>(a, n, st)
-                                                                    : launch_cluster_sort<4>(a, n, st));
+    rc = form.items == 1 ? launch_cluster_sort<1>(a, form.ctas, st)
+                         : (form.items == 2 ? launch_cluster_sort<2>(a, form.ctas, st) : launch_cluster_sort<4>(a, form.ctas, st));
     if (rc) return rc;
   } else {
     int cur = 0;
@@ -674,6 +724,11 @@ int ngram_embed_fwd_mx4(const ngram_embed_plan* plan, const int32_t* tokens, con
 size_t ngram_embedding_workspace_bytes(int64_t max_ids, int64_t D) {
   if (max_ids < 0 || max_ids > INT32_MAX || D < 1 || D > INT32_MAX) return 0;
   return grad_ws(max_ids, D, nullptr).bytes;
+}
+
+int ngram_embedding_sort_ctas(int64_t n, int limit) {
+  if (n < 1 || n > INT32_MAX || limit < 0) return NGRAM_ERR_INVALID_ARG;
+  return cluster_form(n, limit < kClusterCtas ? limit : kClusterCtas).ctas;
 }
 
 int ngram_embedding_fwd(const void* table, const void* table_scales, int table_dtype, int64_t V, int64_t D,

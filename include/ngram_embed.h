@@ -425,6 +425,11 @@ int ngram_embedding_bwd(const int32_t* ids, int64_t n, const void* grad_out, int
                         int64_t grad_stride, int64_t V, int64_t D, float scale, int64_t pad_id,
                         float* d_table, void* workspace, size_t workspace_bytes, void* stream);
 
+/* CTAs of the cluster that sorts the ids of a gradient's n positions, on a device that places
+ * clusters of up to `limit` CTAs (a whole B200: 16); 0: they are sorted in tiles by several
+ * launches. The bits of the gradient are the same. Negative on bad arguments. */
+int ngram_embedding_sort_ctas(int64_t n, int limit);
+
 /* The same gradient as rows, for tables too large for a dense one: *num_rows (device int32)
  * distinct ids, ascending, in rows[0 .. *num_rows), their gradients in grads[u] (fp32 [n x D],
  * written, not added to). Room for n rows; those past *num_rows are left as they were. */

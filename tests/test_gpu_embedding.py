@@ -1,5 +1,9 @@
 """The lookup of one table and its gradient by sorted ids, on the GPU, against plain 64-bit
 definitions on the host."""
+import os
+import subprocess
+import sys
+
 import numpy as np
 import pytest
 import torch
@@ -352,3 +356,25 @@ def test_lookup_of_every_4bit_value_rounds_its_product_once(ne, scale):
         out = torch.full((256, 32), 9.0, dtype=dtype, device="cuda")
         ne.ngram_embedding_fwd(table, None, out, ws, scale=scale)
         assert torch.allclose(out.cpu(), want.to(dtype), rtol=0, atol=0, equal_nan=True)
+
+
+FIRST_CALL = """
+import torch, hashed_gram_embedding_horner_b200 as ne
+n, D, V = 3000, 64, 500
+ids, g = torch.randint(0, V, (n,), dtype=torch.int32, device="cuda"), torch.ones((n, D), device="cuda")
+d, ws = torch.zeros((V, D), device="cuda"), ne.new_embedding_workspace(n, D)
+torch.cuda.synchronize()
+graph = torch.cuda.CUDAGraph()
+with torch.cuda.graph(graph):
+    ne.ngram_embedding_bwd(ids, g, d, ws)
+assert not bool(d.any())
+graph.replay()
+assert torch.equal(d, torch.bincount(ids, minlength=V).float()[:, None].expand(V, D))
+"""
+
+
+def test_gradient_captured_as_a_process_s_first_call():
+    """What a device is asked and told once (shared memory, cluster sizes) may fall into a capture."""
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    r = subprocess.run([sys.executable, "-c", FIRST_CALL], cwd=root, capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0, r.stderr[-2000:]

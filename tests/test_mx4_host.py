@@ -165,3 +165,18 @@ def test_binding_refuses_host_tensors_and_wrong_shapes(ne):
     for none in (None, torch.zeros(64, dtype=torch.uint8)[::2]):
         with pytest.raises(ne.NgramError):
             ne._space(none, -1)
+
+
+@pytest.mark.parametrize("limit,most", [(16, 65536), (15, 32768), (8, 32768), (4, 16384), (1, 4096), (0, 0), (32, 65536)])
+def test_gradient_sort_fits_the_clusters_that_a_device_places(ne, limit, most):
+    """Never more CTAs than the device places, room for every id (4096 a CTA), and the sort in
+    tiles for what does not fit."""
+    for n in (1, 1024, 1025, 4096, 4097, 8192, 8193, 16384, 16385, 32768, 32769, 65536, 65537, 1 << 30):
+        ctas = ne.ngram_embedding_sort_ctas(n, limit)
+        assert ctas <= limit and (ctas == 0) == (n > most)
+        assert ctas == 0 or (n <= 4096 * ctas and ctas & (ctas - 1) == 0)
+    for n, ctas in ((1000, 1), (16384, 16), (16385, 16), (32769, 16)):  # a whole device: few ids a thread
+        assert limit < 16 or ne.ngram_embedding_sort_ctas(n, limit) == ctas
+    for bad in ((0, 16), (-1, 16), (1 << 31, 16), (5, -1)):
+        with pytest.raises(ne.NgramError):
+            ne.ngram_embedding_sort_ctas(*bad)
