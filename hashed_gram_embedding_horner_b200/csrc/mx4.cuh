@@ -839,8 +839,8 @@ __global__ void __launch_bounds__(kMxThreads, 1)
       else umma_commit(drain_bar);
     }
     __syncwarp();
-    // the last commit: every MMA is done and, in CTA 1, every earlier commit's arrival has landed
-    mbar_wait_drain(drain_bar, 0, kWaitLimitNs);
+    // the last commit: every MMA is done
+    if (rank == 0) mbar_wait_drain(drain_bar, 0, kWaitLimitNs);
     __syncwarp();
   } else if (warp >= 4) {
     // ------------------------------------------------------------ epilogue (own 128 rows)
@@ -873,7 +873,13 @@ __global__ void __launch_bounds__(kMxThreads, 1)
 
   tc_fence_before();
   __syncthreads();
-  if (PAIR) cluster_sync();  // no remote arrival or pair MMA is outstanding past this point
+  if (PAIR) {
+    // CTA 1: the last commit's arrival has landed, and so have all earlier ones. Waited for from
+    // the end of its epilogue on: from the kernel's start the limit would cover the whole product.
+    if (rank == 1 && warp == 1) mbar_wait_drain(drain_bar, 0, kWaitLimitNs);
+    __syncthreads();
+    cluster_sync();  // no remote arrival or pair MMA is outstanding past this point
+  }
   if (warp == 1) {
     tc_fence_after();
     if (PAIR) tmem_dealloc_pair(tmem_base, L::kTmemCols);

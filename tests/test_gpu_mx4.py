@@ -406,3 +406,31 @@ def test_products_of_every_form_at_once_on_two_streams(ne):
     for _, _, want, own in calls:
         for out, ws in own:
             assert torch.equal(out, want) and ne.ngram_embed_get_status(ws) == 0
+
+
+def tile_rows(tiles, rows, cols):
+    """Scale bytes of some rows of an array of `cols`, from its tiles."""
+    kt = -(-cols // 128)
+    b = np.arange(cols // 32)
+    at = [(r // 128 * kt + b // 4) * 512 + (r % 32) * 16 + (r // 32 % 4) * 4 + b % 4 for r in rows]
+    return np.stack([tiles[torch.from_numpy(a).cuda()].cpu().numpy() for a in at])
+
+
+def test_product_that_takes_seconds(ne):
+    """A product of more than two seconds, the limit of the kernel's waits for one another, on
+    CTA pairs (a square array by itself): no wait runs out. Some of its rows and columns."""
+    R, K = 131072, 262144
+    assert ne.ngram_mx4_product_form(R, R, K) in (256, 320)
+    gen_d = torch.Generator(device="cuda").manual_seed(3)
+    codes = torch.randint(0, 256, (R, K // 2), dtype=torch.uint8, device="cuda", generator=gen_d)
+    scales = torch.randint(120, 128, (R // 128 * (K // 128) * 512,), dtype=torch.uint8, device="cuda", generator=gen_d)
+    a = ne.Mx4(codes, scales, R, K, ne.MX4_TILES)
+    out, ws = torch.empty((R, R), dtype=BF16, device="cuda"), ne.new_mx4_workspace(R, R, K)
+    ne.ngram_mx4_product(a, a, out, ws)
+    assert ne.ngram_embed_get_status(ws) == 0
+    rows, cols = [0, 129, 70000, R - 1], [0, 63, 64, 255, 256, 40001, R - 2, R - 1]
+    av, bv = (ref.values(ref.unpack(codes[r].cpu().numpy()), tile_rows(scales, r, K)) for r in (rows, cols))
+    got, want = f64(out[rows][:, cols]), av @ bv.T
+    del codes, scales, out, a
+    torch.cuda.empty_cache()
+    assert (np.abs(got - want) <= ref.product_bound(av, bv, ref.BF16_HALF, want)).all()
