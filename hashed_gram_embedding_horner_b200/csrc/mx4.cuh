@@ -697,8 +697,9 @@ __global__ void __launch_bounds__(kMxThreads, 1)
   const int warp = threadIdx.x >> 5;
   const int lane = threadIdx.x & 31;
   const uint32_t rank = PAIR ? cluster_ctarank() : 0u;
-  auto wait = [&](uint32_t bar, uint32_t parity) {
-    return PAIR ? mbar_wait_cluster(bar, parity, abort_flag, p.status) : mbar_wait(bar, parity, abort_flag, p.status);
+  auto wait = [&](uint32_t bar, uint32_t parity, uint64_t limit_ns = kWaitLimitNs) {
+    return PAIR ? mbar_wait_cluster(bar, parity, abort_flag, p.status, limit_ns)
+                : mbar_wait(bar, parity, abort_flag, p.status, limit_ns);
   };
 
   if (threadIdx.x == 0) {
@@ -852,7 +853,11 @@ __global__ void __launch_bounds__(kMxThreads, 1)
       const int acc = L::kAccs == 1 ? 0 : local & 1;
       auto ready = [&] {
         bool got = false;
-        if (lane == 0) got = wait(tfull_bar(acc), (L::kAccs == 1 ? local : local >> 1) & 1u);
+        // a whole tile's k-blocks, ten times what they were measured at (one tile of K = 2^31 takes
+        // 2.36 s)
+        if (lane == 0)
+          got = wait(tfull_bar(acc), (L::kAccs == 1 ? local : local >> 1) & 1u,
+                     kWaitLimitNs + static_cast<uint64_t>(KB) * 4096);
         if (!__shfl_sync(0xffffffffu, got, 0)) return false;
         tc_fence_after();
         return true;

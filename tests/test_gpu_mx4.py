@@ -434,3 +434,34 @@ def test_product_that_takes_seconds(ne):
     del codes, scales, out, a
     torch.cuda.empty_cache()
     assert (np.abs(got - want) <= ref.product_bound(av, bv, ref.BF16_HALF, want)).all()
+
+
+@pytest.mark.parametrize("M", [5, 4])
+def test_product_of_the_longest_rows(ne, M):
+    """K near 2^31: rows of 1 GB, whose one tile takes more than two seconds; offsets past 32
+    bits. Small integers under scales of 1 at a few places, zeros elsewhere: exact."""
+    K = (1 << 31) - 288
+    rng = np.random.default_rng(M)
+    kt = -(-K // 128)
+    parts = []
+    at = [0, 1, 5000, K // 64, K // 32 - 7, K // 32 - 1]  # blocks that are not zero
+    vals = []
+    for rows in (M, 1):
+        codes = torch.zeros((rows, K // 2), dtype=torch.uint8, device="cuda")
+        scales = torch.zeros(kt * 512, dtype=torch.uint8, device="cuda")
+        v = np.zeros((rows, len(at) * 32))
+        for r in range(rows):
+            for j, b in enumerate(at):
+                c = rng.integers(0, 16, (1, 32), dtype=np.uint8)
+                codes[r, b * 16:b * 16 + 16] = torch.from_numpy(ref.pack(c)[0]).cuda()
+                scales[b // 4 * 512 + r * 16 + b % 4] = 127
+                v[r, j * 32:j * 32 + 32] = ref.values(c, np.array([[127]], np.uint8))
+        parts.append(ne.Mx4(codes, scales, rows, K, ne.MX4_TILES))
+        vals.append(v)
+    assert (ne.ngram_mx4_product_form(M, 1, K) == 0) == (M <= 4)
+    out, ws = torch.empty((M, 1), device="cuda"), ne.new_mx4_workspace(M, 1, K)
+    ne.ngram_mx4_product(parts[0], parts[1], out, ws)
+    assert ne.ngram_embed_get_status(ws) == 0
+    assert np.array_equal(f64(out), vals[0] @ vals[1].T)
+    del codes, scales, parts
+    torch.cuda.empty_cache()
