@@ -190,9 +190,10 @@ constexpr Mx4Form kMx4Forms[5] = {{256, 256, 0.32, 1.6, 3.1, 1.5},
 // (40); rows of B much shorter than the 4096 elements that a warp takes at a time leave lanes
 // idle: 50000 x 1024 19 / 33 (12).
 constexpr int kMx4FewRows = 4;
+int mx4_few_rows(int M) { return M < 3 ? M : kMx4FewRows; }  // rows that the kernel for M computes
 double mx4_few_us(int M, int N, int K, int sms) {
   const double elements = static_cast<double>(N) * ((K + 4095) / 4096) * 4096;
-  return elements * (0.13 + 0.04 * M) * 1e-6 * 148 / sms - 1.7;
+  return elements * (0.13 + 0.04 * mx4_few_rows(M)) * 1e-6 * 148 / sms - 1.7;
 }
 int mx4_tile_width(int M, int N, int K, int sms) {
   int width = -1;
@@ -226,8 +227,11 @@ int launch_mx4_gemm(const Mx4GemmParams& prm, const Mx4Operands& o, int sms, cud
   if (sms < 2) return NGRAM_ERR_CUDA;
   const int width = mx4_tile_width(prm.M, prm.N, prm.K, sms);
   if (width == 0)
-    return prm.M == 1 ? launch_mx4_few<1, OutT>(prm, o, st)
-                      : (prm.M == 2 ? launch_mx4_few<2, OutT>(prm, o, st) : launch_mx4_few<4, OutT>(prm, o, st));
+    switch (mx4_few_rows(prm.M)) {
+      case 1: return launch_mx4_few<1, OutT>(prm, o, st);
+      case 2: return launch_mx4_few<2, OutT>(prm, o, st);
+      default: return launch_mx4_few<kMx4FewRows, OutT>(prm, o, st);
+    }
   switch (width) {
     case 320: return launch_mx4_tiles<320, 5, OutT, true>(prm, o, sms, st);
     case 256: return launch_mx4_tiles<256, 5, OutT, true>(prm, o, sms, st);

@@ -180,3 +180,11 @@ def test_gradient_sort_fits_the_clusters_that_a_device_places(ne, limit, most):
     for bad in ((0, 16), (-1, 16), (1 << 31, 16), (5, -1)):
         with pytest.raises(ne.NgramError):
             ne.ngram_embedding_sort_ctas(*bad)
+
+
+def test_three_rows_take_a_warp_a_column_where_four_do(ne):
+    """The kernel of few rows computes three rows as four: as long, so the same choice."""
+    form = ne.ngram_mx4_product_form
+    for N in range(32, 20000, 96):
+        for K in (512, 1024, 2080, 4096, 8192, 16384):
+            assert form(3, N, K) == form(4, N, K), (N, K)
