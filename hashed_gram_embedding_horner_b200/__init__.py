@@ -55,7 +55,7 @@ EXPORTED = [
     "ngram_mx4_product_form",
     "ngram_embed_mx4_workspace_bytes", "ngram_embed_fwd_mx4", "ngram_embed_project_mx4",
     "ngram_embedding_workspace_bytes", "ngram_embedding_fwd", "ngram_embedding_bwd", "ngram_embedding_bwd_rows",
-    "ngram_embedding_sort_ctas",
+    "ngram_embedding_sort_ctas", "ngram_embed_plan_device",
 ]
 
 
@@ -125,6 +125,7 @@ _sig("ngram_embed_selftest_wait_timeout", [_P, _I64, _P])
 _sig("ngram_embed_fwd_static_ws", [_P, _P, _P, _I32, _I64, _P, _P, _P, _P, _P, _P, _P, _P])
 
 _MX = ctypes.POINTER(_Mx4)
+_sig("ngram_embed_plan_device", [_P])
 _sig("ngram_mx4_scale_bytes", [_I64, _I64, ctypes.c_int], _SZ)
 _sig("ngram_mx4_quantize", [_P, ctypes.c_int, _I64, _I64, _I64, _P, _P, ctypes.c_int, _P])
 _sig("ngram_mx4_product_workspace_bytes", [_I64, _I64, _I64], _SZ)
@@ -176,6 +177,7 @@ class Plan:
         self.V_nk, self.dtype = tuple(V_nk), dtype
         self.S = (N - 1) * K
         self.d = D // self.S if self.S else 0
+        self.device = _lib.ngram_embed_plan_device(handle)
 
     def __del__(self):
         h = getattr(self, "handle", None)
@@ -655,6 +657,8 @@ def new_embed_mx4_workspace(plan: Plan, max_tokens: int, device="cuda"):
 
 def _mx4_layer(plan: Plan, n, E0, E_nk, W: Mx4, out, dev):
     """Checks the layer's tensors; returns the array of the sub-tables' addresses."""
+    if plan.device != dev:
+        raise NgramError(f"the plan is for cuda:{plan.device}, out is on cuda:{dev}")
     code, rows, cols, stride = _matrix(out, "out", dev)
     code0, rows0, cols0, stride0 = _matrix(E0, "E0", dev)
     if code != plan.dtype or code0 != plan.dtype or stride != cols or stride0 != cols0:
@@ -678,6 +682,9 @@ def ngram_embed_fwd_mx4(plan: Plan, tokens, seq_offsets, E0, E_nk, W: Mx4, out, 
     dev = out.get_device()
     n, seqs = tokens.numel(), seq_offsets.numel() - 1
     tabs = _mx4_layer(plan, n, E0, E_nk, W, out, dev)
+    if cache:
+        for t in (cache.ring, cache.len, cache.valid_from):
+            _on(dev, "cache", t)
     ws, ws_bytes = _space(workspace, dev)
     rc = _lib.ngram_embed_fwd_mx4(plan.handle, _ids(tokens, "tokens", dev), _ids(seq_offsets, "seq_offsets", dev), seqs, n,
                                   E0.data_ptr(), tabs, W.struct, ctypes.byref(cache.struct) if cache else None,

@@ -1045,6 +1045,8 @@ int ngram_embed_plan_destroy(ngram_embed_plan* plan) {
   return NGRAM_OK;
 }
 
+int ngram_embed_plan_device(const ngram_embed_plan* plan) { return plan ? plan->device : -1; }
+
 int ngram_embed_plan_uses_tensor_cores(const ngram_embed_plan* plan) {
   return plan && plan->variant != kSimt ? 1 : 0;
 }

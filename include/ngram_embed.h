@@ -111,6 +111,9 @@ typedef struct {
  * Returns NGRAM_ERR_INVALID_ARG / NGRAM_ERR_UNSUPPORTED on a bad config. */
 int ngram_embed_plan_create(const ngram_embed_config* cfg, ngram_embed_plan** out);
 int ngram_embed_plan_destroy(ngram_embed_plan* plan);
+/* The device that the plan was built on, which its calls run on and their buffers lie on; -1 if
+ * there was none (or no plan). */
+int ngram_embed_plan_device(const ngram_embed_plan* plan);
 
 /* Device workspace bytes for calls of up to max_tokens tokens: a 33,024-byte head (the
  * status word, then the stream-K arrival counters), the [max_tokens x S] int32 index

@@ -465,3 +465,31 @@ def test_product_of_the_longest_rows(ne, M):
     assert np.array_equal(f64(out), vals[0] @ vals[1].T)
     del codes, scales, parts
     torch.cuda.empty_cache()
+
+
+def test_layer_of_another_device_s_plan_or_cache_is_refused(ne):
+    """Before anything is launched: kernels of one device would read another's memory, or the
+    host's."""
+    V0, D, N, K, V, dtype = LAYERS[2]
+    L = make_layer(ne, 51, V0, D, N, K, V, dtype)
+    tokens, off = torch.zeros(4, dtype=torch.int32, device="cuda"), torch.tensor([0, 4], dtype=torch.int32, device="cuda")
+    idx = torch.zeros((4, L["plan"].S), dtype=torch.int32, device="cuda")
+    ws = ne.new_embed_mx4_workspace(L["plan"], 4)
+    out = torch.full((4, D), 3.0, dtype=dtype, device="cuda")
+    fwd = lambda **kw: ne.ngram_embed_fwd_mx4(L["plan"], tokens, off, L["E0"], L["E"], L["W"], out, ws, **kw)
+    ring = ne.Cache.empty(1, 8)
+    host = ne.Cache.empty(1, 8, device="cpu")
+    for cache in (host, ne.Cache(ring.ring, host.len, ring.valid_from), ne.Cache(ring.ring, ring.len, host.valid_from)):
+        with pytest.raises(ne.NgramError):
+            fwd(cache=cache)
+    here = L["plan"].device
+    assert here == out.get_device()
+    L["plan"].device = here + 1
+    with pytest.raises(ne.NgramError):
+        fwd()
+    with pytest.raises(ne.NgramError):
+        ne.ngram_embed_project_mx4(L["plan"], tokens, idx, L["E0"], L["E"], L["W"], out, ws)
+    assert bool((out == 3.0).all())
+    L["plan"].device = here
+    fwd(cache=ring)
+    assert ne.ngram_embed_get_status(ws) == 0

@@ -188,3 +188,10 @@ def test_three_rows_take_a_warp_a_column_where_four_do(ne):
     for N in range(32, 20000, 96):
         for K in (512, 1024, 2080, 4096, 8192, 16384):
             assert form(3, N, K) == form(4, N, K), (N, K)
+
+
+def test_plan_tells_its_device(ne):
+    import torch
+    plan = _plan(ne)
+    assert plan.device == (torch.cuda.current_device() if torch.cuda.is_available() else -1)
+    assert ne._lib.ngram_embed_plan_device(None) == -1
