@@ -55,7 +55,7 @@ EXPORTED = [
     "ngram_mx4_product_form",
     "ngram_embed_mx4_workspace_bytes", "ngram_embed_fwd_mx4", "ngram_embed_project_mx4",
     "ngram_embedding_workspace_bytes", "ngram_embedding_fwd", "ngram_embedding_bwd", "ngram_embedding_bwd_rows",
-    "ngram_embedding_sort_ctas", "ngram_embed_plan_device",
+    "ngram_embedding_sort_ctas", "ngram_embedding_piece", "ngram_embed_plan_device",
 ]
 
 
@@ -136,6 +136,7 @@ _sig("ngram_embed_fwd_mx4", [_P, _P, _P, _I32, _I64, _P, _MX, _MX, _P, _P, _P, _
 _sig("ngram_embed_project_mx4", [_P, _P, _P, _I64, _P, _MX, _MX, _P, _P, _SZ, _P])
 _sig("ngram_embedding_workspace_bytes", [_I64, _I64], _SZ)
 _sig("ngram_embedding_sort_ctas", [_I64, ctypes.c_int])
+_sig("ngram_embedding_piece", [_I64, _I64])
 _sig("ngram_embedding_fwd", [_P, _P, ctypes.c_int, _I64, _I64, _P, _I64, ctypes.c_float, _I64, _P, ctypes.c_int, _I64,
                              _P, _SZ, _P])
 _sig("ngram_embedding_bwd", [_P, _I64, _P, ctypes.c_int, _I64, _I64, _I64, ctypes.c_float, _I64, _P, _P, _SZ, _P])
@@ -741,6 +742,13 @@ def ngram_embedding_sort_ctas(n: int, limit: int = 16) -> int:
     `limit` CTAs; 0 where they are sorted in tiles."""
     rc = _lib.ngram_embedding_sort_ctas(int(n), int(limit))
     _check(min(rc, 0), "ngram_embedding_sort_ctas")
+    return rc
+
+
+def ngram_embedding_piece(n: int, D: int) -> int:
+    """Sorted positions that one warp of a gradient of n positions sums: 128, 32 or 8."""
+    rc = _lib.ngram_embedding_piece(int(n), int(D))
+    _check(min(rc, 0), "ngram_embedding_piece")
     return rc
 
 

@@ -735,6 +735,11 @@ int ngram_embedding_sort_ctas(int64_t n, int limit) {
   return cluster_form(n, limit < kClusterCtas ? limit : kClusterCtas).ctas;
 }
 
+int ngram_embedding_piece(int64_t n, int64_t D) {
+  if (n < 1 || n > INT32_MAX || D < 1 || D > INT32_MAX) return NGRAM_ERR_INVALID_ARG;
+  return grad_piece(n, D);
+}
+
 int ngram_embedding_fwd(const void* table, const void* table_scales, int table_dtype, int64_t V, int64_t D,
                         const int32_t* ids, int64_t n, float scale, int64_t pad_id, void* out, int out_dtype,
                         int64_t out_stride, void* workspace, size_t workspace_bytes, void* stream) {

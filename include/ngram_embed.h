@@ -432,6 +432,9 @@ int ngram_embedding_bwd(const int32_t* ids, int64_t n, const void* grad_out, int
  * clusters of up to `limit` CTAs (a whole B200: 16); 0: they are sorted in tiles by several
  * launches. The bits of the gradient are the same. Negative on bad arguments. */
 int ngram_embedding_sort_ctas(int64_t n, int limit);
+/* Sorted positions that one warp of a gradient of n positions sums (128, 32 or 8): the sums of
+ * an id's longer runs are added in the order of these pieces. Negative on bad arguments. */
+int ngram_embedding_piece(int64_t n, int64_t D);
 
 /* The same gradient as rows, for tables too large for a dense one: *num_rows (device int32)
  * distinct ids, ascending, in rows[0 .. *num_rows), their gradients in grads[u] (fp32 [n x D],

@@ -378,3 +378,51 @@ def test_gradient_captured_as_a_process_s_first_call():
     root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
     r = subprocess.run([sys.executable, "-c", FIRST_CALL], cwd=root, capture_output=True, text=True, timeout=300)
     assert r.returncode == 0, r.stderr[-2000:]
+
+
+def many_ids(rng, n, V, kind):
+    """`one`: nearly all positions one id, among others before and behind it."""
+    ids = ids_of(rng, n, V, "zipf" if kind == "one" else kind)
+    if kind == "one":
+        ids[rng.random(n) < 0.97] = V // 2
+    return ids
+
+
+PIECES = [  # n, V, D, kind: of all lengths of pieces, sorted in a cluster and in tiles, runs of over 1024 pieces
+    (20000, 3000, 7176, "zipf"), (65536, 5000, 2056, "zipf"), (32768, 4000, 4096, "one"), (70001, 2500, 2040, "zipf"),
+    (150000, 700, 1024, "one"), (600000, 900, 8, "same"), (100000, 300, 64, "one"), (64000, 99, 24, "same"),
+    (9000, 50, 8, "same"), (9100, 50, 16, "one"),
+]
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("n,V,D,kind", PIECES)
+def test_gradient_in_pieces_of_every_length(ne, n, V, D, kind, dtype):
+    """Sums of small integers are exact in any order: equal to the plain sums in 64 bits. With
+    and without padding, as rows and densely."""
+    rng = np.random.default_rng(n + D)
+    ids = torch.from_numpy(many_ids(rng, n, V, kind)).cuda()
+    g = torch.randint(-8, 9, (n, D), dtype=torch.int8, device="cuda", generator=torch.Generator("cuda").manual_seed(n)).to(dtype)
+    ws = ne.new_embedding_workspace(n, D)
+    rows, count = (torch.full((k,), -5, dtype=torch.int32, device="cuda") for k in (n, 1))
+    grads, dense = torch.full((n, D), 4.0, device="cuda"), torch.empty((V, D), device="cuda")
+    for pad in (-1, int(ids[n // 3]), V // 2):
+        keep = ids != pad
+        want = torch.zeros((V, D), dtype=torch.float64, device="cuda").index_add_(0, ids[keep].long(), g[keep].double()) * 0.5
+        used = torch.unique(ids[keep])
+        ne.ngram_embedding_bwd_rows(ids, g, V, rows, count, grads, ws, scale=0.5, pad_id=pad)
+        U = int(count)
+        assert U == len(used) and torch.equal(rows[:U], used)
+        assert torch.equal(grads[:U].double(), want[used.long()])
+        dense.fill_(3.0)
+        ne.ngram_embedding_bwd(ids, g, dense, ws, scale=0.5, pad_id=pad)
+        assert torch.equal(dense.double(), want + 3.0)
+    assert ne.ngram_embed_get_status(ws) == 0
+
+
+def test_gradients_above_take_every_piece_and_sort(ne):
+    forms = {(ne.ngram_embedding_piece(n, D), ne.ngram_embedding_sort_ctas(n) > 0) for n, _, D, _ in PIECES}
+    assert {p for p, _ in forms} == {8, 32, 128} and {(32, False), (128, False), (128, True)} <= forms
+    for kind in ("same", "one"):  # runs over more than 1024 pieces, of every length
+        assert {ne.ngram_embedding_piece(n, D) for n, _, D, k in PIECES
+                if k == kind and 0.97 * n > 1025 * ne.ngram_embedding_piece(n, D)} == {8, 32, 128}

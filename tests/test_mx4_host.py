@@ -195,3 +195,15 @@ def test_plan_tells_its_device(ne):
     plan = _plan(ne)
     assert plan.device == (torch.cuda.current_device() if torch.cuda.is_available() else -1)
     assert ne._lib.ngram_embed_plan_device(None) == -1
+
+
+def test_gradient_pieces(ne):
+    """The longest pieces that leave 4096 warps (1024 for the middle ones) of 256 columns."""
+    for n in (1, 8, 641, 4096, 32767, 32768, 65536, 131072, 524161, 524160, 1 << 30):
+        for D in (8, 136, 256, 264, 2048, 4096, 7176):
+            warps = lambda p: -(-n // p) * -(-D // 256)
+            want = 128 if warps(128) >= 4096 else (32 if warps(32) >= 1024 else 8)
+            assert ne.ngram_embedding_piece(n, D) == want
+    for bad in ((0, 8), (1 << 31, 8), (5, 0), (5, 1 << 31)):
+        with pytest.raises(ne.NgramError):
+            ne.ngram_embedding_piece(*bad)
