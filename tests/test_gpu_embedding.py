@@ -426,3 +426,51 @@ def test_gradients_above_take_every_piece_and_sort(ne):
     for kind in ("same", "one"):  # runs over more than 1024 pieces, of every length
         assert {ne.ngram_embedding_piece(n, D) for n, _, D, k in PIECES
                 if k == kind and 0.97 * n > 1025 * ne.ngram_embedding_piece(n, D)} == {8, 32, 128}
+
+
+def test_lookups_and_gradients_in_flight_at_once(ne):
+    """Two streams, nothing waited for between the calls: lookups and gradients, one side sorted in
+    a cluster and the other in tiles, give the bits of a call alone every time."""
+    rng = np.random.default_rng(33)
+    V, D = 4000, 136
+    table = torch.from_numpy(rng.standard_normal((V, D))).float().cuda()
+    sides = []
+    for n in (60000, 90000):
+        ids = torch.from_numpy(ids_of(rng, n, V, "zipf")).cuda()
+        g = torch.from_numpy(rng.standard_normal((n, D))).float().cuda()
+        own = [dict(out=torch.empty_like(g), rows=torch.zeros(n, dtype=torch.int32, device="cuda"), grads=torch.zeros_like(g),
+                    count=torch.zeros(1, dtype=torch.int32, device="cuda"), dense=torch.zeros((V, D), device="cuda"),
+                    ws=ne.new_embedding_workspace(n, D)) for _ in range(3)]
+        sides.append((ids, g, own))
+
+    def call(side, k, st=None):
+        ids, g, own = sides[side]
+        o = own[k]
+        ne.ngram_embedding_fwd(table, ids, o["out"], o["ws"], scale=1.5, pad_id=1, stream=st)
+        ne.ngram_embedding_bwd_rows(ids, g, V, o["rows"], o["count"], o["grads"], o["ws"], scale=1.5, pad_id=1, stream=st)
+        ne.ngram_embedding_bwd(ids, g, o["dense"], o["ws"], scale=1.5, pad_id=1, stream=st)
+
+    repeats = 10
+    for side in range(2):
+        for _ in range(repeats):
+            call(side, 0)
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    torch.cuda.synchronize()
+    begin, end = ([torch.cuda.Event(enable_timing=True) for _ in range(2)] for _ in range(2))
+    for r in range(repeats):
+        for side, st in enumerate(streams):  # a given stream, and the current one
+            if r == 0:
+                begin[side].record(st)
+            call(side, 1, st)
+            with torch.cuda.stream(st):
+                call(side, 2)
+            if r == repeats - 1:
+                end[side].record(st)
+    torch.cuda.synchronize()
+    assert begin[0].elapsed_time(end[1]) > 0 and begin[1].elapsed_time(end[0]) > 0  # beside one another
+    for _, _, own in sides:
+        U = int(own[0]["count"])
+        for o in own[1:]:
+            assert int(o["count"]) == U and torch.equal(o["rows"][:U], own[0]["rows"][:U])
+            assert torch.equal(o["grads"][:U], own[0]["grads"][:U]) and torch.equal(o["out"], own[0]["out"])
+            assert torch.equal(o["dense"], own[0]["dense"]) and ne.ngram_embed_get_status(o["ws"]) == 0
