@@ -474,3 +474,27 @@ def test_lookups_and_gradients_in_flight_at_once(ne):
             assert int(o["count"]) == U and torch.equal(o["rows"][:U], own[0]["rows"][:U])
             assert torch.equal(o["grads"][:U], own[0]["grads"][:U]) and torch.equal(o["out"], own[0]["out"])
             assert torch.equal(o["dense"], own[0]["dense"]) and ne.ngram_embed_get_status(o["ws"]) == 0
+
+
+def test_lookup_and_quantisation_of_more_rows_than_a_launch(ne):
+    """2^28 rows of 32 columns are a launch's most: the rows at its border and the last ones, a
+    padding id behind it, an id as far as the table goes."""
+    n, D = (1 << 28) + 70, 32
+    q = ne.Mx4.empty(n, D)
+    x = torch.randint(-6, 7, (n, D), dtype=torch.int8, device="cuda").to(BF16)
+    ne.ngram_mx4_quantize(x, q)
+    some = torch.cat([torch.arange(0, 70), torch.arange((1 << 28) - 70, n)]).cuda()
+    codes, scales = ref.quantise(f64(x[some]))
+    assert np.array_equal(q.codes[some].cpu().numpy(), ref.pack(codes)) and np.array_equal(q.scales[some].cpu().numpy(), scales)
+    vals = torch.from_numpy(ref.values(codes, scales)).cuda()
+    ws = ne.new_embedding_workspace(0, D)
+    x.fill_(9.0)
+    pad = (1 << 28) + 3
+    ne.ngram_embedding_fwd(q, None, x, ws, scale=2.0, pad_id=pad)
+    vals[some == pad] = 0
+    assert torch.equal(x[some].double(), vals * 2.0)  # 4 bits times 2: exact in bf16
+    ids = torch.arange(n - 1, -1, -1, dtype=torch.int32, device="cuda")
+    ne.ngram_embedding_fwd(q, ids, x, ws, scale=2.0, pad_id=pad)
+    assert torch.equal(x[n - 1 - some].double(), vals * 2.0) and ne.ngram_embed_get_status(ws) == 0
+    del q, x, ids
+    torch.cuda.empty_cache()
