@@ -4,6 +4,7 @@ import numpy as np
 import pytest
 import torch
 
+import oracle
 from synth import gen
 from tests import mx4_ref as ref
 
@@ -493,3 +494,74 @@ def test_layer_of_another_device_s_plan_or_cache_is_refused(ne):
     L["plan"].device = here
     fwd(cache=ring)
     assert ne.ngram_embed_get_status(ws) == 0
+
+
+MANY_TILES = [  # M, N, K: three tiles and more for some CTA or pair of every form
+    (60000, 60, 64), (60000, 60, 1056), (16384, 1000, 512), (130, 30000, 64), (9000, 1500, 1024), (60000, 190, 64),
+    (16384, 1000, 1024), (34215, 423, 32), (56000, 320, 1056), (54669, 274, 32),
+]
+TILE_ROWS = {320: 256, 256: 256, 192: 128, 128: 128, 64: 128}
+
+
+def tiles_a_worker(ne, M, N, K):
+    """The form of a product and the most tiles that one CTA or pair of it takes."""
+    sms = torch.cuda.get_device_properties(0).multi_processor_count
+    w = ne.ngram_mx4_product_form(M, N, K, sms)
+    tiles = -(-M // TILE_ROWS[w]) * -(-N // w)
+    return w, -(-tiles // (sms * 128 // TILE_ROWS[w]))
+
+
+def gpu_bound(a, b, half, want):
+    """mx4_ref.product_bound on 64-bit tensors of the GPU."""
+    acc = a.shape[1] * 2.0 ** -23 * (a.abs() @ b.abs().T)
+    return acc + half * (want.abs() + acc)
+
+
+@pytest.mark.parametrize("M,N,K", MANY_TILES)
+def test_product_of_several_tiles_a_worker(ne, M, N, K):
+    """Accumulators used again, stages that run on from tile to tile, ragged last tiles."""
+    assert tiles_a_worker(ne, M, N, K)[1] >= 3
+    rng = np.random.default_rng(M + N)
+    a, b = ref.random_mx4(rng, M, K), ref.random_mx4(rng, N, K)
+    A, B = device_mx4(ne, *a, ne.MX4_TILES), device_mx4(ne, *b, ne.MX4_TILES)
+    av, bv = (torch.from_numpy(ref.values(*t)).cuda() for t in (a, b))
+    want = av @ bv.T * 0.5
+    ws = ne.new_mx4_workspace(M, N, K)
+    for dtype in (BF16, F32):
+        out = torch.full((M, N), 7.0, dtype=dtype, device="cuda")
+        ne.ngram_mx4_product(A, B, out, ws, alpha=0.5)
+        assert bool(((out.double() - want).abs() <= gpu_bound(av, bv * 0.5, HALF[dtype], want)).all())
+    assert ne.ngram_embed_get_status(ws) == 0
+
+
+MANY_TILES_LAYERS = [(64, 3, 1, 60000), (512, 3, 2, 14336), (1024, 3, 1, 14336), (320, 3, 1, 56500), (2048, 5, 2, 8192)]  # D, N, K, T
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("D,N,K,T", MANY_TILES_LAYERS)
+def test_layer_of_several_tiles_a_worker(ne, D, N, K, T, dtype):
+    assert tiles_a_worker(ne, T, D, D)[1] >= 3
+    V0, S = 3000, (N - 1) * K
+    V = [1001 + 10 * s for s in range(S)]
+    L = make_layer(ne, D + T, V0, D, N, K, V, dtype)
+    off = gen.offsets_from_lengths([T - 1001, 0, 1, 1000])
+    tokens = np.random.default_rng(T).integers(0, V0, T).astype(np.int32)
+    idx = torch.from_numpy(oracle.hash_indices(V0, N, K, V, oracle.context_windows(N, tokens, off)).astype(np.int64)).cuda()
+    G = torch.cat([torch.from_numpy(e).cuda()[idx[:, s]] for s, e in enumerate(L["E_vals"])], dim=1)
+    W, e0 = torch.from_numpy(L["W_vals"]).cuda(), L["E0"].double()[torch.from_numpy(tokens).cuda().long()]
+    mag = G.abs() @ W.abs().T
+    want = (e0 + G @ W.T) / (S + 1)
+    # as mx4_ref.layer: the sums, the E_0 add, the scale and its product
+    acc = (D * 2.0 ** -23 * mag + 3 * ref.F32_HALF * (mag + e0.abs())) / (S + 1)
+    ws = ne.new_embed_mx4_workspace(L["plan"], T)
+    out = torch.full((T, D), 3.0, dtype=dtype, device="cuda")
+    ne.ngram_embed_fwd_mx4(L["plan"], torch.from_numpy(tokens).cuda(), torch.from_numpy(off).cuda(), L["E0"], L["E"],
+                           L["W"], out, ws)
+    assert ne.ngram_embed_get_status(ws) == 0
+    assert bool(((out.double() - want).abs() <= acc + HALF[dtype] * (want.abs() + acc)).all())
+
+
+def test_sizes_above_give_every_form_three_tiles_a_worker(ne):
+    for sizes in (MANY_TILES, [(T, D, D) for D, _, _, T in MANY_TILES_LAYERS]):
+        took = dict(tiles_a_worker(ne, *s) for s in sizes)
+        assert set(took) == set(TILE_ROWS) and min(took.values()) >= 3
