@@ -565,3 +565,31 @@ def test_sizes_above_give_every_form_three_tiles_a_worker(ne):
     for sizes in (MANY_TILES, [(T, D, D) for D, _, _, T in MANY_TILES_LAYERS]):
         took = dict(tiles_a_worker(ne, *s) for s in sizes)
         assert set(took) == set(TILE_ROWS) and min(took.values()) >= 3
+
+
+def test_products_of_all_forms_in_flight_on_two_streams(ne):
+    """Pairs, single CTAs and the form of few rows beside one another, nothing waited for between
+    the calls: each result has the bits of its call alone."""
+    sizes = [(2300, 2048, 2048), (1280, 4096, 4096), (16384, 1000, 1024), (9000, 1500, 1024), (16384, 1000, 512),
+             (333, 1111, 2080), (1, 4096, 4096), (28600, 318, 1056)]
+    assert {ne.ngram_mx4_product_form(*s) for s in sizes} == {0, *TILE_ROWS}
+    gen_d = torch.Generator(device="cuda").manual_seed(6)
+    calls = []
+    for M, N, K in sizes:
+        a, b = (ne.Mx4(torch.randint(0, 256, (r, K // 2), dtype=torch.uint8, device="cuda", generator=gen_d),
+                       torch.randint(120, 130, (ne._lib.ngram_mx4_scale_bytes(r, K, ne.MX4_TILES),), dtype=torch.uint8,
+                                     device="cuda", generator=gen_d), r, K, ne.MX4_TILES) for r in (M, N))
+        own = [(torch.empty((M, N), dtype=BF16, device="cuda"), ne.new_mx4_workspace(M, N, K)) for _ in range(3)]
+        ne.ngram_mx4_product(a, b, *own[2])
+        calls.append((a, b, own))
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    for rep in range(30):
+        for k in range(len(calls)):
+            for i, st in enumerate(streams):
+                a, b, own = calls[(k * (1 + 2 * i) + rep) % len(calls)]  # each stream in an order of its own
+                ne.ngram_mx4_product(a, b, *own[i], stream=st)
+    torch.cuda.synchronize()
+    for _, _, own in calls:
+        for out, ws in own[:2]:
+            assert torch.equal(out, own[2][0]) and ne.ngram_embed_get_status(ws) == 0
