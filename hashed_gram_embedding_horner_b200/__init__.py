@@ -606,7 +606,7 @@ class Mx4:
 
 
 def ngram_mx4_quantize(x, out: Mx4, stream=None):
-    """Quantise the rows of x (bf16 or f32 [rows, cols], rows may be strided) into `out`."""
+    """Quantise the rows of x (bf16 or f32 [rows, cols], rows may be strided or one row expanded) into `out`."""
     code, rows, cols, stride = _matrix(x, "x", out.device)
     if rows != out.rows or cols != out.cols:
         raise NgramError(f"x is {(rows, cols)}, out {(out.rows, out.cols)}")
@@ -760,7 +760,8 @@ def _f32_dense(t, name, device):
 
 
 def ngram_embedding_bwd(ids, grad_out, d_table, workspace, scale: float = 1.0, pad_id: int = -1, stream=None):
-    """d_table [V, D] (f32) += the lookup's gradient for grad_out [n, D] (bf16 or f32)."""
+    """d_table [V, D] (f32) += the lookup's gradient for grad_out [n, D] (bf16 or f32; rows may be
+    strided or one row expanded)."""
     code, n, D, stride = _matrix(grad_out, "grad_out")
     dev = grad_out.get_device()
     V, cols = _f32_dense(d_table, "d_table", dev)

@@ -71,6 +71,9 @@ struct DeviceScope {
   DeviceScope& operator=(const DeviceScope&) = delete;
 };
 
+// A row stride of an array that is only read: of rows beside one another, or 0, one row for all.
+bool read_stride_ok(int64_t stride, int64_t cols) { return stride == 0 || stride >= cols; }
+
 bool aligned32(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 31u) == 0; }
 
 int device_sms() {
@@ -464,7 +467,7 @@ int embedding_bwd(const int32_t* ids, int64_t n, const void* g, int g_dtype, int
                   void* workspace, size_t workspace_bytes, void* stream) {
   if (n < 0 || n > INT32_MAX || V < 1 || V >= (int64_t(1) << 31) || D < 1 || D > INT32_MAX || !(scale - scale == 0.0f) ||
       (g_dtype != NGRAM_BF16 && g_dtype != NGRAM_F32) || !workspace || (!dense && !count_out) ||
-      (n > 0 && (!ids || !g || !out || (!dense && !rows_out) || g_stride < D)))
+      (n > 0 && (!ids || !g || !out || (!dense && !rows_out) || !read_stride_ok(g_stride, D))))
     return NGRAM_ERR_INVALID_ARG;
   if (D % 8 != 0) return NGRAM_ERR_UNSUPPORTED;
   const int elt = g_dtype == NGRAM_BF16 ? 2 : 4;
@@ -604,7 +607,7 @@ int ngram_mx4_quantize(const void* src, int dtype, int64_t rows, int64_t cols, i
                        void* scales, int layout, void* stream) {
   if (rows < 0 || rows > INT32_MAX || cols < 1 || cols > INT32_MAX || (dtype != NGRAM_BF16 && dtype != NGRAM_F32) ||
       (layout != NGRAM_MX4_ROWS && layout != NGRAM_MX4_TILES) ||
-      (rows > 0 && (!src || !codes || !scales || src_stride < cols)))
+      (rows > 0 && (!src || !codes || !scales || !read_stride_ok(src_stride, cols))))
     return NGRAM_ERR_INVALID_ARG;
   if (cols % kMxBlock != 0) return NGRAM_ERR_UNSUPPORTED;
   if (rows == 0) return NGRAM_OK;

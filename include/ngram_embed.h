@@ -350,7 +350,8 @@ typedef struct {
 /* Bytes of the scales of [rows x cols] in a layout; 0 on bad arguments. */
 size_t ngram_mx4_scale_bytes(int64_t rows, int64_t cols, int layout);
 
-/* Quantise src [rows x cols] (NGRAM_BF16 or NGRAM_F32, row stride src_stride elements):
+/* Quantise src [rows x cols] (NGRAM_BF16 or NGRAM_F32, row stride src_stride elements, at least
+ * cols, or 0 for one row that all rows read):
  *   e    = clamp(floor(log2(max |x| of the block)) - 2 + 127, 0, 254), 0 for a block of zeros;
  *   code = x / 2^(e - 127) rounded to the nearest E2M1 value, ties to even, saturating at 6.
  * A block that holds an infinity or a NaN becomes NaN: e = 255, codes 0. cols must be a
@@ -419,7 +420,8 @@ int ngram_embedding_fwd(const void* table, const void* table_scales, int table_d
 
 /* Its gradient: d_table[v] += scale * sum of grad_out[i] over the positions i with ids[i] = v
  * (d_table [V x D] fp32, D a multiple of 8). grad_out is [n x D] NGRAM_BF16 or NGRAM_F32, row
- * stride grad_stride elements. Rows of grad_out and the gradients are 16-byte aligned. Positions
+ * stride grad_stride elements, at least D, or 0 for one row that all positions share. Rows of
+ * grad_out and the gradients are 16-byte aligned. Positions
  * are sorted by id and summed in fp32 in a fixed order without atomics: equal inputs give equal
  * bits. For a 4-bit table this is the gradient of its master (the straight-through estimate).
  * Ids outside [0, V) count as row 0, as in the lookup.

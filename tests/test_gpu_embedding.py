@@ -498,3 +498,22 @@ def test_lookup_and_quantisation_of_more_rows_than_a_launch(ne):
     assert torch.equal(x[n - 1 - some].double(), vals * 2.0) and ne.ngram_embed_get_status(ws) == 0
     del q, x, ids
     torch.cuda.empty_cache()
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+def test_gradient_and_quantisation_of_one_row_for_all(ne, dtype):
+    """A broadcast row (stride 0), as a mean's gradient is: the same bits as its copies."""
+    rng = np.random.default_rng(71)
+    n, V, D = 700, 40, 160
+    row = torch.from_numpy(rng.standard_normal(D)).to(dtype).cuda()
+    g = row.expand(n, D)
+    ids = ids_of(rng, n, V, "zipf")
+    got = check_rows(ne, ids, g, V, 0.5, -1)
+    want = check_rows(ne, ids, g.contiguous(), V, 0.5, -1)
+    assert got[2] == want[2] and torch.equal(got[1], want[1])
+    for lo in (0, 5):
+        view = torch.cat([row, row])[lo:lo + 128].expand(33, 128)
+        a, b = ne.Mx4.empty(33, 128), ne.Mx4.empty(33, 128)
+        ne.ngram_mx4_quantize(view, a)
+        ne.ngram_mx4_quantize(view.contiguous(), b)
+        assert torch.equal(a.codes, b.codes) and torch.equal(a.scales, b.scales)

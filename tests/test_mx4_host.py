@@ -207,3 +207,15 @@ def test_gradient_pieces(ne):
     for bad in ((0, 8), (1 << 31, 8), (5, 0), (5, 1 << 31)):
         with pytest.raises(ne.NgramError):
             ne.ngram_embedding_piece(*bad)
+
+
+def test_strides_of_arrays_that_are_read(ne):
+    """0, or at least the columns; the refusal that follows (a misaligned array) shows that the
+    stride was let through."""
+    q = lambda st: ne._lib.ngram_mx4_quantize(FAKE, 0, 4, 64, st, ODD, FAKE, 0, None)
+    assert [q(st) for st in (-64, -1, 1, 63)] == [-1] * 4 and [q(st) for st in (0, 64, 65)] == [-3] * 3
+    need = ne._lib.ngram_embedding_workspace_bytes(9, 64)
+    dense = lambda st: ne._lib.ngram_embedding_bwd(FAKE, 9, FAKE, 1, st, 50, 64, 1.0, -1, ODD, FAKE, need, None)
+    rows = lambda st: ne._lib.ngram_embedding_bwd_rows(FAKE, 9, FAKE, 1, st, 50, 64, 1.0, -1, FAKE, FAKE, ODD, FAKE, need, None)
+    for f in (dense, rows):
+        assert [f(st) for st in (-64, -1, 8, 63)] == [-1] * 4 and [f(st) for st in (0, 64, 68)] == [-3] * 3
