@@ -363,8 +363,9 @@ int ngram_mx4_quantize(const void* src, int dtype, int64_t rows, int64_t cols, i
 
 /* out[m][n] = alpha * sum_k A[m][k] B[n][k] for A [M x K] and B [N x K] with scales in tiles:
  * the block-scaled tensor-core product, fp32 sums, rounded once to out_dtype (NGRAM_BF16 or
- * NGRAM_F32). out has a row stride of out_stride elements (any; 16-byte aligned rows are
- * written fastest). K must be a multiple of 32.
+ * NGRAM_F32). out has a row stride of out_stride elements, N or more (16-byte aligned rows are
+ * written fastest). K must be a multiple of 32, alpha finite. The least workspace is a status
+ * word's, which calls at the same time may share.
  *   workspace  >= ngram_mx4_product_workspace_bytes(M, N, K); its head as for a plan's
  *              workspace (zeroed once; status word). The device that owns it is the call's. */
 size_t ngram_mx4_product_workspace_bytes(int64_t M, int64_t N, int64_t K);
@@ -401,14 +402,15 @@ int ngram_embed_project_mx4(const ngram_embed_plan* plan, const int32_t* tokens,
                             void* stream);
 
 /* ---- one table: lookup and gradient ----
- * out[i] = scale * table[ids[i]] for n int32 ids (device), in fp32, rounded once to out_dtype.
+ * out[i] = scale * table[ids[i]] for n int32 ids (device), in fp32, rounded once to out_dtype;
+ * scale finite.
  *   table        [V x D] NGRAM_BF16, NGRAM_F32, or NGRAM_MX4 codes with table_scales by rows
  *                (NULL otherwise), 16-byte aligned; D a multiple of 8 (NGRAM_MX4: of 32)
  *   ids          NULL: ids[i] = i, n <= V (a whole table read back)
  *   pad_id       positions whose id is pad_id get a row of zeros and the gradient skips them;
  *                negative: none
- *   out          [n x D] NGRAM_BF16 or NGRAM_F32, row stride out_stride elements (rows and base
- *                16-byte aligned)
+ *   out          [n x D] NGRAM_BF16 or NGRAM_F32, row stride out_stride elements, D or more (rows
+ *                and base 16-byte aligned)
  *   workspace    >= ngram_embedding_workspace_bytes(0, D): the status word's head; the device
  *                that owns it is the call's. An id outside [0, V) that is not pad_id reads row 0
  *                and sets NGRAM_STATUS_BAD_TOKEN. */
@@ -425,7 +427,8 @@ int ngram_embedding_fwd(const void* table, const void* table_scales, int table_d
  * are sorted by id and summed in fp32 in a fixed order without atomics: equal inputs give equal
  * bits. For a 4-bit table this is the gradient of its master (the straight-through estimate).
  * Ids outside [0, V) count as row 0, as in the lookup.
- *   workspace  >= ngram_embedding_workspace_bytes(n, D) */
+ *   workspace  >= ngram_embedding_workspace_bytes(n, D), of its own for each of the calls that
+ *              may run at the same time (the sort and the pieces' sums lie in it) */
 int ngram_embedding_bwd(const int32_t* ids, int64_t n, const void* grad_out, int grad_dtype,
                         int64_t grad_stride, int64_t V, int64_t D, float scale, int64_t pad_id,
                         float* d_table, void* workspace, size_t workspace_bytes, void* stream);
