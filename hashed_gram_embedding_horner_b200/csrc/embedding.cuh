@@ -598,8 +598,9 @@ __global__ void __launch_bounds__(256, kJoinBlocksPerSm) grad_join_kernel(const 
 // exchange their digit counts, and every position is stored straight into its place in the
 // shared memory of the CTA that the place belongs to. Positions past n carry the largest key,
 // so they stay last. The gradient of 1000 / 32768 / 65536 rows of eight columns
-// takes 14 / 31 / 42 us in a graph, against 32 / 45 / 48 with the tiled sort and the numbering
-// kernels, which are ten launches more.
+// takes 14 / 32 / 42 us in a graph, against 28 / 45 / 49 with the tiled sort and the numbering
+// kernels, which are ten launches more (15 / 32 / 42 against 45 / 67 / 71 one call after another).
+// Devices that place no cluster of the size take the tiled sort too (cluster_limit).
 
 constexpr int kClusterThreads = 1024;
 constexpr int kClusterMaxItems = 4;  // positions a thread: 1, 2 or 4, as few as hold n

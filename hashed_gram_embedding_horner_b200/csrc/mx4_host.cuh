@@ -1,11 +1,12 @@
 // Host side of the 4-bit table operators and of the table lookup with its gradient
 // (included by ngram_embed.cu after its own helpers).
 //
-// All but the tiled sort are programmatic dependent launches: a kernel's set-up runs while the one
-// before ends, and it waits for all of that before its first global access. In graphs: one
-// token's projection 9.8 -> 9.0 us, a decode step's layer 24.3 -> 22.8, the gradient of 32768 rows
-// 111 -> 103; one call after another, for the first kernels of the calls: the step's layer
-// 24.4 -> 22.1, the gradients of 32768 and 641 rows 101.3 -> 99.1, 18.7 -> 16.9. The product, the
+// All but the sort in tiles and the numbering after it are programmatic dependent launches: a
+// kernel's set-up runs while the one before ends, and it waits for all of that before its first
+// global access. With them (and with plain launches), in graphs: one token's projection 6.7 us
+// (7.2), a decode step's layer 19.9 (21.1), the gradients of 32768 rows of 4096 columns 95.4
+// (101.4) and of 641 rows 14.5 (16.1); one call after another: 10.9 (11.8), 20.6 (25.1), 96.8
+// (107.0), 17.2 (24.0). The product, the
 // lookup and the join do not let their own dependents start early: the projection of 1280 tokens
 // took 17.5 us for 16.9, the gradient 118 for 97.
 #pragma once
