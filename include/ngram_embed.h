@@ -362,8 +362,8 @@ int ngram_mx4_quantize(const void* src, int dtype, int64_t rows, int64_t cols, i
                        void* codes, void* scales, int layout, void* stream);
 
 /* out[m][n] = alpha * sum_k A[m][k] B[n][k] for A [M x K] and B [N x K] with scales in tiles:
- * the block-scaled tensor-core product, fp32 sums, rounded once to out_dtype (NGRAM_BF16 or
- * NGRAM_F32). out has a row stride of out_stride elements, N or more (16-byte aligned rows are
+ * the block-scaled tensor-core product, fp32 sums (a partial sum beyond fp32's range is an
+ * infinity), rounded once to out_dtype (NGRAM_BF16 or NGRAM_F32). out has a row stride of out_stride elements, N or more (16-byte aligned rows are
  * written fastest). K must be a multiple of 32, alpha finite. The least workspace is a status
  * word's, which calls at the same time may share.
  *   workspace  >= ngram_mx4_product_workspace_bytes(M, N, K); its head as for a plan's
